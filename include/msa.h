@@ -334,6 +334,89 @@ int msa_sparse_prefill(int32_t n_layers, int32_t B, int32_t T, int32_t Hq, const
                        const uint16_t* loc_k, const uint16_t* loc_v, const int32_t* loc_len,
                        int32_t max_loc, float scale, float* out, void* stream);
 
+/* -------------------------------------------------------------- paged local cache
+ *
+ * [P5 推理全流程: the memory KV is fixed while the local KV grows token by token]  The
+ * local K/V rows of many sequences in pages of one pool, so a row is written once when
+ * its token comes and never moved:
+ *
+ *   k_pages, v_pages  [n_layers][n_pages][page_tokens][8][128] bf16, page_tokens a power
+ *                     of two up to MSA_MAX_PAGE_TOKENS
+ *   page_table        [B][max_pages] int32: local row r of sequence b is row
+ *                     r % page_tokens of page page_table[b][r / page_tokens], in every layer
+ *   q_off             [B + 1] int32, ascending: the new tokens of sequence b are the packed
+ *                     rows q_off[b] .. q_off[b + 1]) of k_new, v_new, q and the outputs (a
+ *                     sequence may have none); packed rows from q_off[B] on are padding:
+ *                     never used, and their output rows are left as they were
+ *   kv_len            [B] int32: local rows of sequence b, its new tokens INCLUDED (they are
+ *                     the last ones): new token i of n has local row kv_len[b] - n + i
+ *
+ * Both calls take the same q_off, kv_len and page_table.  Limits: B <= MSA_MAX_SEQS, n_q <=
+ * MSA_MAX_NEW_TOKENS, max_pages * page_tokens <= MSA_MAX_LOCAL_ROWS, n_pages * page_tokens <
+ * 2^31 (UNSUPPORTED beyond).  n_q == 0 enqueues nothing (k_new, v_new, q, out may be NULL). */
+#define MSA_MAX_SEQS 2048
+#define MSA_MAX_PAGE_TOKENS 1024
+#define MSA_MAX_NEW_TOKENS (1 << 22)
+#define MSA_MAX_LOCAL_ROWS (1 << 30)
+
+/* Appends the new tokens' K/V to the cache and turns K and Q to their positions on the way.
+ * [P2 5.2 Step 1: k_norm, q_norm, rotary positions; P2 3.3.1, P5: the query's positions start
+ * at an offset]  Per new token with local row r, position p = pos_off[b] + r:  k is scaled per
+ * head by w_k / sqrt(mean(k^2) + eps) (w_k given) and its pairs (e, e + 64) turned by the angle
+ * p * theta^(-e/64); q likewise with w_q; v is stored as it is.  fp32 arithmetic, angles
+ * reduced in fp64, one rounding to bf16.
+ *
+ *   k_new, v_new  [n_layers][n_q][8][128] bf16
+ *   q, q_out      [n_layers][n_q][Hq][128] bf16, Hq in {8, 16, 32, 64}; q_out may be q.  q may
+ *                 be NULL (only the cache is written; Hq, w_q and q_out are not read)
+ *   pos_off       [B] int32, or NULL for 0
+ *   w_k, w_q      [n_layers][128] bf16, or NULL for no norm
+ *
+ * Tokens with a local row below 0 (kv_len[b] smaller than the sequence's new tokens), past the
+ * page table's row, or on a page outside [0, n_pages) are not stored; their q is turned all the
+ * same.  Two tokens of one call must not have the same row of the same page.  Errors: NULL
+ * pointers, sizes < 1, page_tokens no power of two, eps < 0, theta <= 0 or not finite (SHAPE), the
+ * limits above (UNSUPPORTED). */
+int msa_paged_append(int32_t n_layers, int32_t B, int32_t n_q, int32_t Hq, const uint16_t* k_new,
+                     const uint16_t* v_new, const uint16_t* q, const int32_t* q_off, const int32_t* kv_len,
+                     const int32_t* pos_off, const int32_t* page_table, int32_t max_pages, int32_t page_tokens,
+                     int32_t n_pages, const uint16_t* w_k, const uint16_t* w_q, float eps, float theta,
+                     uint16_t* k_pages, uint16_t* v_pages, uint16_t* q_out, void* stream);
+
+/* Attention of the new tokens over [memory context ; paged local rows], for sequences that share
+ * a context.  [P1 架构; P2 5.2; P5 推理全流程]  The sequences grp_off[g] .. grp_off[g + 1]) form
+ * group g; new token i of sequence b of group g sees the group's memory rows 0 .. ctx_len[l][g])
+ * and b's local rows 0 .. kv_len[b] - n + i (causal, as msa_sparse_prefill).  The memory rows,
+ * and the first pre_len[g] local rows where that is given, are read once for all sequences of
+ * the group: these local rows must lie in the same pages in all of them (the first sequence's
+ * table is read).  One new token a sequence is the decode, many are the prefill; both may be
+ * mixed in one call.
+ *
+ *   q             [n_layers][n_q][Hq][128] bf16, Hq in {8, 16, 32, 64}
+ *   grp_off       [n_groups + 1] int32, ascending from 0 to B; not read (may be NULL) when
+ *                 n_groups == B: then every sequence is its own group
+ *   ctx_k, ctx_v  [n_layers][n_groups][max_ctx][8][128] bf16 (as msa_gather_ctx writes them for
+ *                 n_groups queries); ctx_len [n_layers][n_groups] int32.  NULL when max_ctx == 0
+ *   pre_len       [n_groups] int32 or NULL
+ *   scale         positive and finite
+ *   out           [n_layers][n_q][Hq][128], fp32 (out_bf16 = 0) or bf16 (out_bf16 = 1); zero for
+ *                 a token that sees no row
+ *
+ * Scores, softmax and sums in fp32.  With fp32 output the probabilities enter the P.V product as
+ * a bf16 high part plus a bf16 residual (~16 significant bits), with bf16 output as one bf16 value
+ * (its rounding is the size of the output's own).  Rows a token does not see never reach its
+ * output, infinities and NaN in them included.  Lengths are clamped to [0, max_ctx] and
+ * [0, max_pages * page_tokens], page numbers to [0, n_pages).  A workspace serves one call at a
+ * time.  Errors: NULL pointers, sizes < 1, n_groups > B, Hq % 8 != 0, page_tokens no power of
+ * two, scale (SHAPE), the limits above (UNSUPPORTED), small workspace. */
+size_t msa_paged_attend_workspace_size(int32_t n_layers, int32_t B, int32_t n_groups, int32_t n_q, int32_t Hq);
+int msa_paged_attend(int32_t n_layers, int32_t B, int32_t n_groups, int32_t n_q, int32_t Hq, const uint16_t* q,
+                     const int32_t* q_off, const int32_t* grp_off, const uint16_t* ctx_k, const uint16_t* ctx_v,
+                     const int32_t* ctx_len, int32_t max_ctx, const uint16_t* k_pages, const uint16_t* v_pages,
+                     int32_t n_pages, int32_t page_tokens, const int32_t* page_table, int32_t max_pages,
+                     const int32_t* kv_len, const int32_t* pre_len, float scale, int32_t out_bf16, void* out,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

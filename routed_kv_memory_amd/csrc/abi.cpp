@@ -431,3 +431,101 @@ MSA_API int msa_sparse_prefill(int32_t n_layers, int32_t B, int32_t T, int32_t H
                                         max_loc, scale, out, as_stream(stream)),
                     "msa_sparse_prefill");
 }
+
+// --------------------------------------------------------------- paged local cache
+
+namespace {
+
+// log2 of a page's tokens, -1 when it is not a power of two within the limits
+int page_shift_of(int32_t page_tokens) {
+  if (page_tokens < 1 || page_tokens > MSA_MAX_PAGE_TOKENS || (page_tokens & (page_tokens - 1))) return -1;
+  return __builtin_ctz((unsigned)page_tokens);
+}
+
+// the sizes that the append and the attention share
+int check_paged_sizes(const char* fn, int32_t n_layers, int32_t B, int32_t n_q, int32_t max_pages,
+                      int32_t page_tokens, int32_t n_pages) {
+  if (n_layers < 1 || B < 1 || n_q < 0 || max_pages < 1 || n_pages < 1 || page_shift_of(page_tokens) < 0)
+    return fail(MSA_ERR_SHAPE, "%s: n_layers=%d B=%d n_q=%d max_pages=%d page_tokens=%d n_pages=%d", fn, n_layers, B,
+                n_q, max_pages, page_tokens, n_pages);
+  if (n_layers > 65535) return fail(MSA_ERR_UNSUPPORTED, "%s: n_layers > 65535", fn);
+  if (B > MSA_MAX_SEQS) return fail(MSA_ERR_UNSUPPORTED, "%s: B=%d > %d", fn, B, MSA_MAX_SEQS);
+  if (n_q > MSA_MAX_NEW_TOKENS) return fail(MSA_ERR_UNSUPPORTED, "%s: n_q=%d > %d", fn, n_q, MSA_MAX_NEW_TOKENS);
+  if ((int64_t)max_pages * page_tokens > MSA_MAX_LOCAL_ROWS || (int64_t)n_pages * page_tokens > INT32_MAX)
+    return fail(MSA_ERR_UNSUPPORTED, "%s: %d or %d pages of %d tokens are too many", fn, max_pages, n_pages, page_tokens);
+  return MSA_OK;
+}
+
+bool head_group_ok(int32_t Hq) { return Hq == 8 || Hq == 16 || Hq == 32 || Hq == 64; }
+
+int check_heads(const char* fn, int32_t Hq) {
+  if (Hq < 1 || Hq % MSA_HEADS != 0) return fail(MSA_ERR_SHAPE, "%s: Hq=%d", fn, Hq);
+  if (!head_group_ok(Hq)) return fail(MSA_ERR_UNSUPPORTED, "%s: Hq=%d (supported: 8, 16, 32, 64)", fn, Hq);
+  return MSA_OK;
+}
+
+}  // namespace
+
+MSA_API int msa_paged_append(int32_t n_layers, int32_t B, int32_t n_q, int32_t Hq, const uint16_t* k_new,
+                             const uint16_t* v_new, const uint16_t* q, const int32_t* q_off, const int32_t* kv_len,
+                             const int32_t* pos_off, const int32_t* page_table, int32_t max_pages,
+                             int32_t page_tokens, int32_t n_pages, const uint16_t* w_k, const uint16_t* w_q,
+                             float eps, float theta, uint16_t* k_pages, uint16_t* v_pages, uint16_t* q_out,
+                             void* stream) {
+  if (!q_off || !kv_len || !page_table || !k_pages || !v_pages || (n_q > 0 && (!k_new || !v_new)) || (q && !q_out))
+    return fail(MSA_ERR_NULL, "msa_paged_append: null pointer");
+  if (!all_aligned16({k_new, v_new, q, w_k, w_q, k_pages, v_pages, q ? q_out : nullptr}))
+    return fail(MSA_ERR_SHAPE, "msa_paged_append: bf16 arrays must be 16-byte aligned");
+  int st = check_paged_sizes("msa_paged_append", n_layers, B, n_q, max_pages, page_tokens, n_pages);
+  if (!st && q) st = check_heads("msa_paged_append", Hq);
+  if (st) return st;
+  if (!(eps >= 0.f) || !(eps < __builtin_inff()) || !(theta > 0.f) || !(theta < __builtin_inff()))
+    return fail(MSA_ERR_SHAPE, "msa_paged_append: eps=%g theta=%g", (double)eps, (double)theta);
+  if (n_q == 0) return MSA_OK;
+  return hip_status(msa::launch_append(n_layers, B, n_q, Hq, k_new, v_new, q, q_off, kv_len, pos_off, page_table,
+                                       max_pages, page_shift_of(page_tokens), n_pages, w_k, w_q, eps, theta, k_pages,
+                                       v_pages, q_out, as_stream(stream)),
+                    "msa_paged_append");
+}
+
+MSA_API size_t msa_paged_attend_workspace_size(int32_t n_layers, int32_t B, int32_t n_groups, int32_t n_q,
+                                               int32_t Hq) {
+  if (n_layers < 1 || n_layers > 65535 || B < 1 || B > MSA_MAX_SEQS || n_groups < 1 || n_groups > B || n_q < 0 ||
+      n_q > MSA_MAX_NEW_TOKENS || !head_group_ok(Hq))
+    return 0;
+  return msa::attend_workspace_bytes(n_layers, B, n_groups, n_q, Hq) + 256;
+}
+
+MSA_API int msa_paged_attend(int32_t n_layers, int32_t B, int32_t n_groups, int32_t n_q, int32_t Hq, const uint16_t* q,
+                             const int32_t* q_off, const int32_t* grp_off, const uint16_t* ctx_k,
+                             const uint16_t* ctx_v, const int32_t* ctx_len, int32_t max_ctx, const uint16_t* k_pages,
+                             const uint16_t* v_pages, int32_t n_pages, int32_t page_tokens,
+                             const int32_t* page_table, int32_t max_pages, const int32_t* kv_len,
+                             const int32_t* pre_len, float scale, int32_t out_bf16, void* out, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (!q_off || !page_table || !kv_len || !k_pages || !v_pages || !workspace || (n_q > 0 && (!q || !out)))
+    return fail(MSA_ERR_NULL, "msa_paged_attend: null pointer");
+  if (max_ctx > 0 && (!ctx_k || !ctx_v || !ctx_len)) return fail(MSA_ERR_NULL, "msa_paged_attend: null memory context");
+  if (!all_aligned16({q, max_ctx > 0 ? ctx_k : nullptr, max_ctx > 0 ? ctx_v : nullptr, k_pages, v_pages, out}))
+    return fail(MSA_ERR_SHAPE, "msa_paged_attend: q, K/V and out must be 16-byte aligned");
+  int st = check_paged_sizes("msa_paged_attend", n_layers, B, n_q, max_pages, page_tokens, n_pages);
+  if (!st) st = check_heads("msa_paged_attend", Hq);
+  if (st) return st;
+  if (n_groups < 1 || n_groups > B || max_ctx < 0)
+    return fail(MSA_ERR_SHAPE, "msa_paged_attend: n_groups=%d B=%d max_ctx=%d", n_groups, B, max_ctx);
+  if (n_groups < B && !grp_off) return fail(MSA_ERR_NULL, "msa_paged_attend: null grp_off");
+  if (max_ctx > MSA_MAX_LOCAL_ROWS) return fail(MSA_ERR_UNSUPPORTED, "msa_paged_attend: max_ctx=%d", max_ctx);
+  if (!(scale > 0.f) || !(scale < __builtin_inff()))
+    return fail(MSA_ERR_SHAPE, "msa_paged_attend: scale=%g must be positive and finite", (double)scale);
+  if (out_bf16 != 0 && out_bf16 != 1) return fail(MSA_ERR_SHAPE, "msa_paged_attend: out_bf16=%d", out_bf16);
+  const size_t need = msa_paged_attend_workspace_size(n_layers, B, n_groups, n_q, Hq);
+  if (workspace_bytes < need)
+    return fail(MSA_ERR_WORKSPACE, "msa_paged_attend: workspace %zu < %zu bytes", workspace_bytes, need);
+  if (n_q == 0) return MSA_OK;
+  void* ws = reinterpret_cast<void*>(align256(reinterpret_cast<size_t>(workspace)));
+  return hip_status(msa::launch_attend(n_layers, B, n_groups, n_q, Hq, q, q_off, n_groups < B ? grp_off : nullptr, ctx_k,
+                                       ctx_v, ctx_len, max_ctx, k_pages, v_pages, n_pages, page_shift_of(page_tokens),
+                                       page_table, max_pages, kv_len, pre_len, scale, out_bf16 == 1, out, ws,
+                                       as_stream(stream)),
+                    "msa_paged_attend");
+}

@@ -129,6 +129,21 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
+// Sequence of packed token t: the number of offsets off[1 .. B] that are <= t (off ascending), B for a
+// token behind the last sequence.  The whole wave searches: 64 offsets a step, one step up to 64
+// sequences, two up to 4,096.
+__device__ __forceinline__ int32_t seq_of_token(const int32_t* __restrict__ off, int32_t B, int32_t t, int lane) {
+  int32_t lo = 0, len = B;                  // the answer lies in [lo, lo + len]
+  while (len > 0) {
+    const int32_t step = (len + 63) >> 6;
+    const int32_t i = (lane + 1) * step;    // ends of up to 64 blocks of `step` offsets
+    const int n = __popcll(__ballot(i <= len && off[lo + (i <= len ? i : len)] <= t));
+    lo += n * step;
+    len = step > 1 ? min(step - 1, len - n * step) : 0;
+  }
+  return lo;
+}
+
 // Per-document max of block scores held one per lane in lanes [0, n) of a wave
 // (lanes >= n pass doc = -1).  Blocks of a document are contiguous, so a
 // segmented suffix max inside each run leaves the run's max in its first lane,

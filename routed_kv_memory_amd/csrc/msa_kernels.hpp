@@ -56,4 +56,20 @@ hipError_t launch_prefill(int32_t L, int32_t B, int32_t T, int32_t Hq, const uin
                           const uint16_t* loc_v, const int32_t* loc_len, int32_t max_loc, float scale, float* out,
                           hipStream_t s);
 
+// append.hip
+hipError_t launch_append(int32_t L, int32_t B, int32_t n_q, int32_t Hq, const uint16_t* k_new, const uint16_t* v_new,
+                         const uint16_t* q, const int32_t* q_off, const int32_t* kv_len, const int32_t* pos_off,
+                         const int32_t* page_table, int32_t max_pages, int32_t page_shift, int32_t n_pages,
+                         const uint16_t* w_k, const uint16_t* w_q, float eps, float theta, uint16_t* k_pages,
+                         uint16_t* v_pages, uint16_t* q_out, hipStream_t s);
+
+// attend.hip
+size_t attend_workspace_bytes(int32_t L, int32_t B, int32_t n_groups, int32_t n_q, int32_t Hq);
+hipError_t launch_attend(int32_t L, int32_t B, int32_t n_groups, int32_t n_q, int32_t Hq, const uint16_t* q,
+                         const int32_t* q_off, const int32_t* grp_off, const uint16_t* ctx_k, const uint16_t* ctx_v,
+                         const int32_t* ctx_len, int32_t max_ctx, const uint16_t* k_pages, const uint16_t* v_pages,
+                         int32_t n_pages, int32_t page_shift, const int32_t* page_table, int32_t max_pages,
+                         const int32_t* kv_len, const int32_t* pre_len, float scale, bool bf16_out, void* out,
+                         void* ws, hipStream_t s);
+
 }  // namespace msa
