@@ -357,7 +357,7 @@ int msa_sparse_prefill(int32_t n_layers, int32_t B, int32_t T, int32_t Hq, const
 #define MSA_MAX_SEQS 2048
 #define MSA_MAX_PAGE_TOKENS 1024
 #define MSA_MAX_NEW_TOKENS (1 << 22)
-#define MSA_MAX_LOCAL_ROWS (1 << 29)
+#define MSA_MAX_LOCAL_ROWS (1 << 22)
 
 /* Appends the new tokens' K/V to the cache and turns K and Q to their positions on the way.
  * [P2 5.2 Step 1: k_norm, q_norm, rotary positions; P2 3.3.1, P5: the query's positions start
