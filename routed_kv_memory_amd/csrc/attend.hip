@@ -10,16 +10,16 @@
 // tokens, or alone in its group, makes one job over everything; the others of a group make one job of
 // all their tokens over the shared rows and one job each over its own rows.  Memory rows are visible to
 // all columns of a job; of the local rows a column sees those below its own limit.  Lengths are on the
-// device, so each workgroup forms the list itself (a few loads and a scan over the jobs, in LDS)
-// and finds its part of it; the host only bounds the numbers of workgroups.
+// device, so each workgroup forms the list itself (a few loads and two scans over the jobs, in LDS)
+// and finds its part of it; the host only bounds the number of workgroups.
 //
-// Three kernels:
-// - attend_stream_kernel, jobs of up to 16 columns, bound by the rows' bytes: a wave takes one KV head
-//   and streams rows through a tile of its own in LDS, without barriers;
-// - attend_tile_kernel, more columns, bound by the matrix cores and the softmax's vector work: 4 waves
-//   take one head and share each tile of 32 rows, 32 columns a wave;
-// - attend_join_kernel, where a column's rows were cut into parts; what is whole in one part has been
-//   written by the kernel that computed it.
+// One kernel (attend_kernel) whose workgroups are of two kinds, so that both fill the chip together:
+// - jobs of up to 16 columns are bound by the rows' bytes: a wave takes one KV head and streams rows
+//   through a tile of its own in LDS, without barriers (attend_streams);
+// - more columns are bound by the matrix cores and the softmax's vector work: 4 waves take one head and
+//   share each tile of 32 rows, 32 columns a wave (attend_item).
+// attend_join_kernel joins where a column's rows were cut into parts; what is whole in one part has been
+// written by the workgroup that computed it.
 // In both, S^T = K . Q^T is computed with K as the A operand and the columns as the B operand
 // (registers), so a lane holds scores of one column and the softmax needs only exchanges between the
 // lane groups of a wave; for O^T += V^T . P^T the MFMA's k axis is taken in the order in which the scores
@@ -37,24 +37,26 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kStreamCols = 16;           // columns of a wave of the stream kernel, most of its jobs
-constexpr int kCols = 32;                 // columns of a wave of the tile kernel
+constexpr int kStreamCols = 16;           // columns of a wave that streams, and most of such a job
+constexpr int kCols = 32;                 // columns of a wave that shares tiles
 // A sequence of more columns than this does not share its group's rows: parts of so many columns cost
 // more to write and join than the rows cost to read again.
 constexpr int kAlone = 512;
-constexpr int kWide = kWaves * kCols;     // columns of a workgroup of the tile kernel
+constexpr int kWide = kWaves * kCols;     // columns of a workgroup of the second kind
 constexpr int kSets = kHeads / kWaves;    // head sets of a streamed job: streams of rows it makes
 constexpr int kStreamRows = 32;           // rows of a streamed tile
 constexpr int kTileRows = 32;             // rows of a shared tile
-// bf16 per staged row of the stream kernel: 16-byte reads of 16 K rows, and transposed reads of 16 dims of
+// bf16 per staged row of a stream: 16-byte reads of 16 K rows, and transposed reads of 16 dims of
 // 8 V rows, meet every LDS bank once
 constexpr int kKStride = kDim + 8;
 constexpr int kVStride = kDim + 16;
 constexpr int kMaxSeqs = 2048;            // MSA_MAX_SEQS
 constexpr int kSegments = 32;             // pieces of streams a workgroup lists at a time
-// Workgroups of one call: two of either kernel fit a CU (registers, LDS).
-constexpr int kStreamWgs = 512;
-constexpr int kTileItems = 512;
+// Two workgroups fit a CU (registers, LDS): 512 fill the chip.  A layer gets its share of them, but at
+// least kBothWgs where there are jobs of both kinds: items come in eights (the heads), and a handful of
+// eights would not split the work evenly.
+constexpr int kWgs = 512;
+constexpr int kBothWgs = 56;
 
 struct AttendArgs {
   int32_t B, n_groups, n_q, Hq, G, g_shift, max_ctx, n_pages, page_shift, max_pages;
@@ -66,10 +68,9 @@ struct AttendArgs {
   const int32_t *page_table, *kv_len, *pre_len;
   float scale2;                           // scale * log2 e
   void* out;
-  int32_t stream_wgs, tile_items;         // workgroups of the stream kernel, items aimed at by the other; a layer
+  int32_t wgs, both_wgs;                  // workgroups aimed at in a layer: jobs of one kind, of both
   int32_t unit_cols;                      // columns of a part in the workspace
-  int32_t stream_units, max_units;        // parts of one layer: the stream kernel's, all
-  uint32_t* tile_count;                   // [L]: the tile kernel's items; the stream kernel counts them
+  int32_t stream_units, max_units;        // parts of one layer: streamed ones, all
   int4* desc;                             // [L][n_q][own rows, shared rows][2]: where a token's parts are
   float2* ml;                             // [L][max_units][unit_cols]: maximum (log2 units) and sum
   float* acc;                             // [L][max_units][unit_cols][128]
@@ -84,25 +85,24 @@ struct Job {
 
 // The lengths of one layer, clamped, in LDS (in the memory of the tiles, before those come).
 struct Lengths {
-  int32_t *off, *len, *grp;       // [kMaxSeqs + 1] each
-  int32_t *clen, *pre;            // [kMaxSeqs]
+  int32_t *off, *grp;             // [kMaxSeqs + 1]
+  int32_t *len, *clen, *pre;      // [kMaxSeqs]
   // bit b: sequence b shares rows with none before it (first of its group, alone, or behind one that is)
   uint32_t* start;                // [kMaxSeqs / 32 + 1]
-  uint32_t* sums;                 // [kWaves][2], and kWaves floats
+  uint32_t* sums;                 // [8][kWaves]
 };
 constexpr int kStartWords = kMaxSeqs / 32 + 1;
-constexpr int kLengthsA = 3 * (kMaxSeqs + 4) * 4;                              // bytes
-constexpr int kLengthsB = 2 * kMaxSeqs * 4 + (kStartWords + 7 & ~7) * 4 + kWaves * 3 * 4;
+constexpr int kStage = 1024;              // 16-byte words of a stage of shared tiles (below)
 
-__device__ __forceinline__ Lengths lengths_in(void* a, void* b) {
+__device__ __forceinline__ Lengths lengths_in(u32x4* a, u32x4* b, u32x4* c, u32x4* d) {
   Lengths n;
-  n.off = static_cast<int32_t*>(a);
-  n.len = n.off + kMaxSeqs + 4;
-  n.grp = n.len + kMaxSeqs + 4;
-  n.clen = static_cast<int32_t*>(b);
-  n.pre = n.clen + kMaxSeqs;
-  n.start = reinterpret_cast<uint32_t*>(n.pre + kMaxSeqs);
-  n.sums = n.start + (kStartWords + 7 & ~7);
+  n.off = reinterpret_cast<int32_t*>(a);
+  n.len = reinterpret_cast<int32_t*>(b);
+  n.pre = n.len + kMaxSeqs;
+  n.clen = reinterpret_cast<int32_t*>(c);
+  n.grp = reinterpret_cast<int32_t*>(d);
+  n.start = reinterpret_cast<uint32_t*>(n.off + kMaxSeqs + 4);
+  n.sums = n.start + kStartWords + 3;
   return n;
 }
 
@@ -233,25 +233,27 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
   return v;
 }
 
-// Inclusive sums over the workgroup's threads of two counts; their totals in `all`.
-__device__ __forceinline__ void scan2(const Lengths& n, uint32_t& x, uint32_t& y, uint32_t* all, int tid) {
+// Inclusive sums over the workgroup's threads of two counts, and their totals; `slot`: 0 or 1, the scans of one
+// plan use different memory, so each needs one barrier.
+__device__ __forceinline__ void scan2(const Lengths& n, int slot, uint32_t& x, uint32_t& y, uint32_t* all, int tid) {
   const int lane = tid & 63, wave = tid >> 6;
+  uint32_t* sums = n.sums + 2 * kWaves * slot;
   x = wave_scan(x);
   y = wave_scan(y);
   if (lane == 63) {
-    n.sums[2 * wave] = x;
-    n.sums[2 * wave + 1] = y;
+    sums[2 * wave] = x;
+    sums[2 * wave + 1] = y;
   }
   __syncthreads();
   all[0] = all[1] = 0;
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
     if (w < wave) {
-      x += n.sums[2 * w];
-      y += n.sums[2 * w + 1];
+      x += sums[2 * w];
+      y += sums[2 * w + 1];
     }
-    all[0] += n.sums[2 * w];
-    all[1] += n.sums[2 * w + 1];
+    all[0] += sums[2 * w];
+    all[1] += sums[2 * w + 1];
   }
 }
 
@@ -492,12 +494,97 @@ __device__ __forceinline__ void describe(const AttendArgs& a, const Job& x, cons
   d[1] = make_int4(head_step, part_step, col, x.split);
 }
 
-// ------------------------------------------------------------------ up to 16 columns
+// ------------------------------------------------------------------ who does what
 //
-// A job makes two streams of rows, one for each set of 4 heads (a wave each).  All streams of a layer
-// are laid end to end and cut into equal shares, one for each workgroup: every workgroup has the same
+// Streamed jobs make two streams of rows each, one for each set of 4 heads (a wave each).  All streams of
+// a layer are laid end to end and cut into equal shares, one for each workgroup: every one has the same
 // number of tiles whatever the lengths are, and one start.  A share holds pieces of one or more
 // streams; a piece is one part of its columns.
+//
+// The other jobs make items: a column block of 128, one head, a chunk of the rows.  A job's rows are cut
+// into its share of the workgroups, rounded down, so that they all run at once, but into chunks of
+// eight tiles at least.  The items come first (workgroups start in order), and of a job those of the last
+// column blocks, whose tokens see the most rows; heads fastest (workgroups go to the 8 XCDs in turn: a
+// head's rows stay in one L2).
+
+__device__ __forceinline__ bool streamed(const Job& x) { return x.cols <= kStreamCols; }
+
+// Chunks of an item job's rows; `aim` is workgroups per tile of work.
+__device__ __forceinline__ int32_t chunks_of(const Job& x, float aim) {
+  const int32_t t = tiles_of(x, kTileRows);
+  return max(1, min(t / 8, (int32_t)((float)t * aim)));
+}
+__device__ __forceinline__ int32_t items_of(const Job& x) { return (x.cols + kWide - 1) / kWide * kHeads; }
+
+struct Plan {
+  int32_t j0, j1;                 // this thread's jobs
+  uint32_t tiles, streams;        // of streamed jobs before them
+  uint32_t items, units;          // items, and those that are parts, before them
+  uint32_t all_tiles, all_items, share, shares;    // tiles of a share, shares
+  float aim;
+};
+
+__device__ __forceinline__ Plan make_plan(const AttendArgs& a, const Lengths& n, int tid) {
+  Plan p;
+  const int32_t nj = a.grp_off ? 2 * a.B : a.B, per = (nj + kThreads - 1) / kThreads;
+  p.j0 = min(nj, tid * per);
+  p.j1 = min(nj, p.j0 + per);
+  // tiles of a layer's streams fit 32 bits: 2 x 4,096 streams of at most 2 x 2^17 tiles.  Work of the
+  // items: fp32 sum of whole numbers, in the same order in every workgroup
+  uint32_t tiles = 0, streams = 0, all[2];
+  float work = 0.f;
+  for (int32_t j = p.j0; j < p.j1; ++j) {
+    const Job x = job_of(a, n, j);
+    if (x.cols == 0) continue;
+    if (streamed(x)) {
+      tiles += kSets * tiles_of(x, kStreamRows);
+      streams += kSets;
+    } else {
+      work += (float)tiles_of(x, kTileRows) * (float)items_of(x);
+    }
+  }
+  p.tiles = tiles;
+  p.streams = streams;
+  work = wave_sum(work);
+  float* sums = reinterpret_cast<float*>(n.sums + 4 * kWaves);
+  if ((tid & 63) == 0) sums[tid >> 6] = work;
+  scan2(n, 0, tiles, streams, all, tid);
+  p.tiles = tiles - p.tiles;
+  p.streams = streams - p.streams;
+  p.all_tiles = all[0];
+  work = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) work += sums[w];
+  p.all_items = p.items = p.units = 0;
+  p.aim = 0.f;
+  p.shares = a.wgs;
+  if (work > 0.f) {                               // uniform
+    // a streamed tile is 4 heads' rows, a shared one is one head's: both take their bytes' time, or as long
+    const float streams_work = 4.f * (float)p.all_tiles;
+    const int32_t wgs = p.all_tiles ? a.both_wgs : a.wgs;
+    // 2^-10 below: the roundings of the sum
+    p.aim = wgs * (1.f - 0x1p-10f) / (work + streams_work);
+    uint32_t items = 0, units = 0;
+    for (int32_t j = p.j0; j < p.j1; ++j) {
+      const Job x = job_of(a, n, j);
+      if (x.cols == 0 || streamed(x)) continue;
+      const int32_t nch = chunks_of(x, p.aim);
+      const uint32_t k = nch * items_of(x);
+      items += k;
+      if (x.shared || x.split || nch > 1) units += k;
+    }
+    p.items = items;
+    p.units = units;
+    scan2(n, 1, items, units, all, tid);
+    p.items = items - p.items;
+    p.units = units - p.units;
+    p.all_items = all[0];
+    p.shares = max((int32_t)(streams_work * p.aim), wgs - (int32_t)min(p.all_items, (uint32_t)wgs));
+    p.shares = max(p.shares, 1u);
+  }
+  p.share = max(1u, (p.all_tiles + p.shares - 1) / p.shares);
+  return p;
+}
 
 struct Segment {
   Job x;
@@ -509,79 +596,20 @@ struct Segment {
   Parts parts;
 };
 
-// Chunks that the rows of a tile job are cut into: its share of the items aimed at, rounded down, so that they
-// all run at once; `aim` is items per tile.  Chunks of eight tiles at least.
-__device__ __forceinline__ int32_t tile_chunks(const Job& x, float aim) {
-  const int32_t t = tiles_of(x, kTileRows);
-  return max(1, min(t / 8, (int32_t)((float)t * aim)));
-}
-__device__ __forceinline__ int32_t tile_items_of(const Job& x) { return (x.cols + kWide - 1) / kWide * kHeads; }
-
-// Over this thread's jobs [j0, j1): items aimed at per tile of work.  fp32 sums of whole numbers, in the same
-// order in every workgroup; 2^-10 below the aim for their roundings.  Has a barrier.
-__device__ __forceinline__ float tile_aim(const AttendArgs& a, const Lengths& n, int32_t j0, int32_t j1, int tid) {
-  float work = 0.f;
-  for (int32_t j = j0; j < j1; ++j) {
-    const Job x = job_of(a, n, j);
-    if (x.cols > kStreamCols) work += (float)tiles_of(x, kTileRows) * (float)tile_items_of(x);
-  }
-  work = wave_sum(work);
-  float* sums = reinterpret_cast<float*>(n.sums) + 2 * kWaves;
-  if ((tid & 63) == 0) sums[tid >> 6] = work;
-  __syncthreads();
-  work = 0.f;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) work += sums[w];
-  return a.tile_items * (1.f - 0x1p-10f) / fmaxf(work, 1.f);
-}
-
-// Items of the tile kernel in this layer (by one workgroup of the stream kernel, which runs before it).
-__device__ __forceinline__ void count_tile_items(const AttendArgs& a, const Lengths& n, int32_t j0, int32_t j1, int64_t layer,
-                                                 int tid) {
-  const float aim = tile_aim(a, n, j0, j1, tid);
-  uint32_t items = 0, none = 0, all[2];
-  for (int32_t j = j0; j < j1; ++j) {
-    const Job x = job_of(a, n, j);
-    if (x.cols > kStreamCols) items += tile_chunks(x, aim) * tile_items_of(x);
-  }
-  scan2(n, items, none, all, tid);
-  __syncthreads();
-  if (tid == 0) a.tile_count[layer] = all[0];
-}
-
-// The jobs of at most 16 columns whose streams reach into the workgroup's share, from tile `from` of
-// the layer's on: up to kSegments pieces into `seg`, their number in n_seg[0]; returns where the list ends.
-__device__ __forceinline__ uint32_t list_segments(const AttendArgs& a, const Lengths& n, Segment* seg, uint32_t* n_seg,
-                                                  int64_t layer, uint32_t from, int tid) {
-  if (tid < 3) n_seg[tid] = 0;
-  load_lengths(a, n, layer, tid);
-  const int32_t nj = a.grp_off ? 2 * a.B : a.B;
-  const int32_t per = (nj + kThreads - 1) / kThreads, j0 = min(nj, tid * per), j1 = min(nj, j0 + per);
-  // tiles of a layer fit 32 bits: 2 x 4,096 streams of at most 2 x 2^17 tiles
-  uint32_t tiles = 0, streams = 0, all[2];
-  for (int32_t j = j0; j < j1; ++j) {
-    const Job x = job_of(a, n, j);
-    if (x.cols == 0 || x.cols > kStreamCols) continue;
-    tiles += kSets * tiles_of(x, kStreamRows);
-    streams += kSets;
-  }
-  const uint32_t my_tiles = tiles, my_streams = streams;
-  scan2(n, tiles, streams, all, tid);
-  if (blockIdx.x == gridDim.x - 1 && from == 0) {     // the last share is the shortest
-    __syncthreads();
-    count_tile_items(a, n, j0, j1, layer, tid);
-  }
-  const uint32_t share = max(1u, (all[0] + a.stream_wgs - 1) / a.stream_wgs);
-  const uint64_t begin = (uint64_t)blockIdx.x * share;
-  if (begin >= all[0]) return 0;
+// The pieces of streams in share `number`, from tile `from` of the layer's on: up to kSegments into `seg`, their
+// number in n_seg[0]; returns where the list ends.
+__device__ __forceinline__ uint32_t list_segments(const AttendArgs& a, const Lengths& n, const Plan& p, Segment* seg,
+                                                  uint32_t* n_seg, uint32_t number, uint32_t from) {
+  const uint32_t share = p.share;
+  const uint64_t begin = (uint64_t)number * share;
+  if (begin >= p.all_tiles) return 0;
   from = max(from, (uint32_t)begin);
-  const uint32_t to = min((uint32_t)begin + share, all[0]);
+  const uint32_t to = min((uint32_t)begin + share, p.all_tiles);
   auto walk = [&](auto&& f) __attribute__((always_inline)) {
-    uint32_t u = tiles - my_tiles, s = streams - my_streams;
-    if (u >= to || tiles <= from) return;
-    for (int32_t j = j0; j < j1; ++j) {
+    uint32_t u = p.tiles, s = p.streams;
+    for (int32_t j = p.j0; j < p.j1 && u < to; ++j) {
       const Job x = job_of(a, n, j);
-      if (x.cols == 0 || x.cols > kStreamCols) continue;
+      if (x.cols == 0 || !streamed(x)) continue;
       const uint32_t t = tiles_of(x, kStreamRows);
       for (int set = 0; set < kSets; ++set, u += t, ++s)
         if (u < to && u + t > from) f(x, set, u, t, s);
@@ -614,7 +642,7 @@ __device__ __forceinline__ uint32_t list_segments(const AttendArgs& a, const Len
     }
     const bool direct = whole && !x.shared && !x.split;
     if (direct) g.parts.first[0] = g.parts.first[1] = -1;
-    g.slot = direct ? -1 : (int32_t)(blockIdx.x + s);
+    g.slot = direct ? -1 : (int32_t)(number + s);
     // only offsets that are not ascending make more parts than there is room for
     if (g.slot >= 0 && kWaves * (g.slot + 1) > a.stream_units) g.x.cols = 0;
     atomicMax(n_seg, k + 1);
@@ -623,6 +651,52 @@ __device__ __forceinline__ uint32_t list_segments(const AttendArgs& a, const Len
   __syncthreads();
   return n_seg[0] < kSegments ? to : n_seg[2];
 }
+
+struct Item {
+  Job x;
+  int32_t valid, nch, tile0, tile1;     // chunks of the job's tiles, this item's tiles
+  int32_t head, col0, blocks;           // first column, column blocks (1, 2 or 4)
+  int32_t unit, first;                  // its first part (-1: writes the output), first chunk and head
+  Parts parts;
+};
+
+__device__ __forceinline__ void find_item(const AttendArgs& a, const Lengths& n, const Plan& p, Item& it, uint32_t id, int tid) {
+  if (tid == 0) it.valid = 0;
+  __syncthreads();
+  uint32_t at = p.items, u = p.units;
+  for (int32_t j = p.j0; j < p.j1 && at <= id; ++j) {
+    const Job x = job_of(a, n, j);
+    if (x.cols == 0 || streamed(x)) continue;
+    const int32_t nch = chunks_of(x, p.aim), ncb = items_of(x) / kHeads;
+    const uint32_t k = nch * ncb * kHeads;
+    const bool parts = x.shared || x.split || nch > 1;
+    if (id < at + k) {
+      const int32_t i = (int32_t)(id - at), t = tiles_of(x, kTileRows);
+      const int32_t chunk = i / kHeads % nch, xb = i / kHeads / nch, len = (t + nch - 1) / nch;
+      it.x = x;
+      it.nch = nch;
+      it.head = i % kHeads;
+      it.col0 = (ncb - 1 - xb) * kWide;
+      it.blocks = x.cols - it.col0 <= kCols ? 1 : (x.cols - it.col0 <= 2 * kCols ? 2 : 4);
+      it.tile0 = min(t, chunk * len);
+      it.tile1 = min(t, it.tile0 + len);
+      it.first = chunk == 0 && it.head == 0;
+      it.unit = parts ? (int32_t)(a.stream_units + kWaves * (u + i)) : -1;
+      for (int v = 0; v < kSets; ++v) {
+        it.parts.first[v] = parts ? (int32_t)(a.stream_units + kWaves * (u + xb * nch * kHeads + v * kWaves)) : -1;
+        it.parts.parts[v] = nch;
+      }
+      // only offsets that are not ascending make more parts than there is room for
+      it.valid = !parts || a.stream_units + (int64_t)kWaves * (u + i + 1) <= a.max_units;
+      break;
+    }
+    at += k;
+    if (parts) u += k;
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------------ up to 16 columns
 
 // 32 rows in the wave's tile: K rows while the scores are formed, then V rows; `then` once these are in.
 template <int PARTS, bool CAREFUL, typename Then>
@@ -661,25 +735,21 @@ __device__ __forceinline__ void attend_rows(uint16_t* tile, const u32x4* pv, con
                                st.o[d]);
 }
 
+// A share of the streams; `tile` is the wave's.
 template <bool BF16_OUT>
-__global__ void __launch_bounds__(kThreads, 2)
-attend_stream_kernel(const AttendArgs a) {
+__device__ __forceinline__ void attend_streams(const AttendArgs& a, const Lengths& n, Plan p, Segment* seg, uint32_t* n_seg,
+                                               uint16_t* tile, uint32_t number, int64_t layer, int tid) {
   constexpr int PARTS = BF16_OUT ? 1 : 2;
-  constexpr int kTile = kStreamRows * kVStride;
-  constexpr int kBytes = kWaves * kTile * 2 > kLengthsA + kLengthsB ? kWaves * kTile * 2 : kLengthsA + kLengthsB;
-  __shared__ __align__(16) char mem[kBytes];
-  __shared__ Segment seg[kSegments];
-  __shared__ uint32_t n_seg[3];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t layer = blockIdx.y;
-  const Lengths n = lengths_in(mem, mem + kLengthsA);
-  uint16_t* tile = reinterpret_cast<uint16_t*>(mem) + wave * kTile;
+  static_assert(kStage * 16 >= kStreamRows * kVStride * 2, "a stage holds a wave's tile");
+  const int lane = tid & 63, wave = tid >> 6;
   // rows by whole 16-lane groups: load i brings rows 4 i + g, dims 8 j .. 8 j + 7
   const int j = lane & 15, g = lane >> 4;
   auto uni = [](int32_t v) { return __builtin_amdgcn_readfirstlane(v); };
 
   for (uint32_t from = 0;;) {
-    const uint32_t reached = list_segments(a, n, seg, n_seg, layer, from, tid);
+    if (tid < 3) n_seg[tid] = 0;
+    __syncthreads();
+    const uint32_t reached = list_segments(a, n, p, seg, n_seg, number, from);
     const int32_t ns = uni((int32_t)n_seg[0]);
     __syncthreads();                              // the lengths' memory becomes the tiles'
 
@@ -809,84 +879,22 @@ attend_stream_kernel(const AttendArgs a) {
       const int32_t slot = uni(seg[s].slot);
       write_state<BF16_OUT>(a, st, rows4_sum(st.l), y, layer, slot < 0 ? -1 : kWaves * slot + wave, lane);
     }
+    if (ns < kSegments) return;                   // uniform
     from = reached;
     __syncthreads();
-    if (ns < kSegments) return;                   // uniform
+    load_lengths(a, n, layer, tid);
+    p = make_plan(a, n, tid);
   }
 }
 
 // ------------------------------------------------------------------ more columns
 
-struct Item {
-  Job x;
-  int32_t valid, nch, tile0, tile1;     // chunks of the job's tiles, this item's tiles
-  int32_t head, col0, blocks;           // first column, column blocks (1, 2 or 4)
-  int32_t unit, first;                  // its first part (-1: writes the output), first chunk and head
-  Parts parts;
-};
-
-// Fills `it` with this workgroup's item.  Items of a job: column blocks from the last (whose tokens see
-// the most rows), chunks of rows, heads fastest (workgroups go to the 8 XCDs in turn: a head's rows
-// stay in one L2).
-__device__ __forceinline__ void find_item(const AttendArgs& a, const Lengths& n, Item& it, int64_t layer, int tid) {
-  if (tid == 0) it.valid = 0;
-  load_lengths(a, n, layer, tid);
-  const int32_t nj = a.grp_off ? 2 * a.B : a.B;
-  const int32_t per = (nj + kThreads - 1) / kThreads, j0 = min(nj, tid * per), j1 = min(nj, j0 + per);
-  const float aim = tile_aim(a, n, j0, j1, tid);
-  uint32_t items = 0, units = 0, all[2];
-  for (int32_t j = j0; j < j1; ++j) {
-    const Job x = job_of(a, n, j);
-    if (x.cols <= kStreamCols) continue;
-    const int32_t nch = tile_chunks(x, aim);
-    const uint32_t k = nch * tile_items_of(x);
-    items += k;
-    if (x.shared || x.split || nch > 1) units += k;
-  }
-  const uint32_t my_items = items, my_units = units;
-  scan2(n, items, units, all, tid);
-  const uint32_t id = blockIdx.x;
-  if (id >= items - my_items && id < items) {
-    uint32_t at = items - my_items, u = units - my_units;
-    for (int32_t j = j0; j < j1; ++j) {
-      const Job x = job_of(a, n, j);
-      if (x.cols <= kStreamCols) continue;
-      const int32_t nch = tile_chunks(x, aim), ncb = (x.cols + kWide - 1) / kWide;
-      const uint32_t k = nch * ncb * kHeads;
-      const bool parts = x.shared || x.split || nch > 1;
-      if (id < at + k) {
-        const int32_t i = (int32_t)(id - at), t = tiles_of(x, kTileRows);
-        const int32_t chunk = i / kHeads % nch, xb = i / kHeads / nch, len = (t + nch - 1) / nch;
-        it.x = x;
-        it.nch = nch;
-        it.head = i % kHeads;
-        it.col0 = (ncb - 1 - xb) * kWide;
-        it.blocks = x.cols - it.col0 <= kCols ? 1 : (x.cols - it.col0 <= 2 * kCols ? 2 : 4);
-        it.tile0 = min(t, chunk * len);
-        it.tile1 = min(t, it.tile0 + len);
-        it.first = chunk == 0 && it.head == 0;
-        it.unit = parts ? (int32_t)(a.stream_units + kWaves * (u + i)) : -1;
-        for (int v = 0; v < kSets; ++v) {
-          it.parts.first[v] = parts ? (int32_t)(a.stream_units + kWaves * (u + xb * nch * kHeads + v * kWaves)) : -1;
-          it.parts.parts[v] = nch;
-        }
-        // only offsets that are not ascending make more parts than there is room for
-        it.valid = !parts || a.stream_units + (int64_t)kWaves * (u + i + 1) <= a.max_units;
-        break;
-      }
-      at += k;
-      if (parts) u += k;
-    }
-  }
-  __syncthreads();
-}
-
-// A stage of the tile kernel holds 32 K rows, then 32 V rows, 16 chunks of 16 bytes each, as the direct
+// A stage holds 32 K rows, then 32 V rows, 16 chunks of 16 bytes each, as the direct
 // global -> LDS loads write them: lane l of load i brings chunk (l & 15) of row 4 i + (l >> 4).  The
 // chunks of a row are permuted by the lanes' source addresses, so that fragment reads meet every bank
 // once: chunk x of K row r lies at x ^ (r & 15) (16 rows, one chunk each), of V row r at
 // x ^ 4 (r & 3) (4 rows, 4 chunks each).
-constexpr int kStage = 2 * kTileRows * 16;        // u32x4
+static_assert(kStage == 2 * kTileRows * 16, "K rows and V rows");
 constexpr int kStages = 4;
 
 typedef __attribute__((address_space(1))) const void* gptr_t;
@@ -943,29 +951,20 @@ __device__ __forceinline__ void attend_stage(const u32x4* stage, const StageRead
   }
 }
 
+struct ItemShared {
+  Item item;
+  int32_t most[kWaves];                   // local rows that a wave's columns see
+  float m[kWaves][kCols], l[kWaves][kCols];
+};
+
+// An item.  An array for each stage, so that the compiler sees which one an access touches.
 template <bool BF16_OUT>
-__global__ void __launch_bounds__(kThreads, 2)
-attend_tile_kernel(const AttendArgs a) {
+__device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& n, ItemShared& z, u32x4* stage0, u32x4* stage1,
+                                            u32x4* stage2, u32x4* stage3, int64_t layer, int tid) {
   constexpr int PARTS = BF16_OUT ? 1 : 2;
-  // an array for each stage, so that the compiler sees which one an access touches
-  __shared__ u32x4 stage0[kStage], stage1[kStage], stage2[kStage], stage3[kStage];
-  __shared__ Item item;
-  __shared__ int32_t s_most[kWaves];                 // local rows that a wave's columns see
-  __shared__ float s_m[kWaves][kCols], s_l[kWaves][kCols];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t layer = blockIdx.y;
+  const int lane = tid & 63, wave = tid >> 6;
   const int c = lane & 31, h = lane >> 5;
-  if (blockIdx.x >= a.tile_count[layer]) return;     // uniform
-  Lengths n = lengths_in(stage0, stage2);
-  n.len = reinterpret_cast<int32_t*>(stage1);
-  n.grp = reinterpret_cast<int32_t*>(stage3);
-  static_assert(sizeof(stage0) >= (kMaxSeqs + 1) * 4, "the lengths fit");
-  n.pre = n.len + kMaxSeqs;
-  n.start = reinterpret_cast<uint32_t*>(n.grp + kMaxSeqs + 4);
-  n.sums = n.start + (kStartWords + 7 & ~7);
-  find_item(a, n, item, layer, tid);
-  if (!item.valid) return;                           // uniform
-  const Item& it = item;
+  const Item& it = z.item;
   auto uni = [](int32_t v) { return __builtin_amdgcn_readfirstlane(v); };
   const Job x = it.x;
   // fewer column blocks than waves: `share` waves take a block's columns and the tiles in turn
@@ -995,13 +994,13 @@ attend_tile_kernel(const AttendArgs a) {
   }
   if (it.first && turn == 0 && y.live && h == 0 && (c & (a.G - 1)) == 0)
     describe(a, x, y, layer, it.parts, it.unit < 0 ? 0 : cb, kWaves, kWaves * kHeads, c);
-  if (lane == 0) s_most[wave] = most;
+  if (lane == 0) z.most[wave] = most;
   __syncthreads();                                   // the lengths' memory becomes the tiles'
 
   const int32_t jc = uni(x.c), p0 = uni(x.p0), seq = uni(x.seq), nctx = (jc + kTileRows - 1) / kTileRows;
   int32_t wg_most = 0;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) wg_most = max(wg_most, s_most[w]);
+  for (int w = 0; w < kWaves; ++w) wg_most = max(wg_most, z.most[w]);
   wg_most = uni(wg_most);
   tile1 = min(tile1, nctx + (wg_most + kTileRows - 1) / kTileRows);
 
@@ -1091,35 +1090,63 @@ attend_tile_kernel(const AttendArgs a) {
   float l = halves_sum(st.l);
   if (share > 1) {             // join the states of a block's waves, in the first of them
     auto state_of = [&](int w) { return reinterpret_cast<float*>(w == 1 ? stage1 : (w == 2 ? stage2 : stage3)); };
-    static_assert(sizeof(stage0) >= kCols * kDim * sizeof(float), "a wave's state fits");
+    static_assert(kStage * 16 >= kCols * kDim * 4, "a wave's state fits");
     if (turn > 0) {
       if (h == 0) {
-        s_m[wave][c] = st.m;
-        s_l[wave][c] = l;
+        z.m[wave][c] = st.m;
+        z.l[wave][c] = l;
       }
 #pragma unroll
       for (int d = 0; d < 4; ++d)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<float4*>(state_of(wave) + c * kDim + 32 * d + 8 * i + 4 * h) =
+          *reinterpret_cast<float4*>(state_of(wave) + 4 * (c + kCols * (8 * d + 2 * i + h))) =
               make_float4(st.o[d][4 * i], st.o[d][4 * i + 1], st.o[d][4 * i + 2], st.o[d][4 * i + 3]);
     }
     __syncthreads();
     if (turn > 0) return;
     for (int w = wave + blocks; w < kWaves; w += blocks) {
       const float* o = state_of(w);
-      const float m = fmaxf(st.m, s_m[w][c]), base = m == -__builtin_huge_valf() ? 0.f : m;
-      const float f = __builtin_amdgcn_exp2f(st.m - base), g = __builtin_amdgcn_exp2f(s_m[w][c] - base);
+      const float m = fmaxf(st.m, z.m[w][c]), base = m == -__builtin_huge_valf() ? 0.f : m;
+      const float f = __builtin_amdgcn_exp2f(st.m - base), g = __builtin_amdgcn_exp2f(z.m[w][c] - base);
       st.m = m;
-      l = l * f + s_l[w][c] * g;
+      l = l * f + z.l[w][c] * g;
 #pragma unroll
       for (int d = 0; d < 4; ++d)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          st.o[d][r] = st.o[d][r] * f + g * o[c * kDim + 32 * d + 8 * (r >> 2) + 4 * h + (r & 3)];
+          st.o[d][r] = st.o[d][r] * f + g * o[4 * (c + kCols * (8 * d + 2 * (r >> 2) + h)) + (r & 3)];
     }
   }
   write_state<BF16_OUT>(a, st, l, y, layer, unit < 0 ? -1 : unit + cb, lane);
+}
+
+template <bool BF16_OUT>
+__global__ void __launch_bounds__(kThreads, 2)
+attend_kernel(const AttendArgs a) {
+  __shared__ u32x4 stage0[kStage], stage1[kStage], stage2[kStage], stage3[kStage];
+  __shared__ union {
+    ItemShared item;
+    struct {
+      Segment seg[kSegments];
+      uint32_t n_seg[3];
+    } streams;
+  } sh;
+  const int tid = threadIdx.x;
+  const int64_t layer = blockIdx.y;
+  const Lengths n = lengths_in(stage0, stage1, stage2, stage3);
+  load_lengths(a, n, layer, tid);
+  const Plan p = make_plan(a, n, tid);
+  const uint32_t id = blockIdx.x;
+  if (id < p.all_items) {                         // uniform
+    find_item(a, n, p, sh.item.item, id, tid);
+    if (sh.item.item.valid) attend_item<BF16_OUT>(a, n, sh.item, stage0, stage1, stage2, stage3, layer, tid);
+  } else if (id - p.all_items < p.shares) {
+    const int wave = tid >> 6;
+    u32x4* tile = wave == 0 ? stage0 : (wave == 1 ? stage1 : (wave == 2 ? stage2 : stage3));
+    attend_streams<BF16_OUT>(a, n, p, sh.streams.seg, sh.streams.n_seg, reinterpret_cast<uint16_t*>(tile), id - p.all_items,
+                             layer, tid);
+  }
 }
 
 // Joins the parts of a token's own rows and of its group's shared rows: four dims of one query head
@@ -1197,41 +1224,36 @@ attend_join_kernel(const AttendArgs a, int32_t per) {
   }
 }
 
-// Bounds for one layer.  Streamed pieces: one for each share and one more for each stream.  A tile job of
-// n > 16 columns has 8 ceil(n / 128) items a chunk, at most n / 2 (8 at 17, 16 at 129) and 8 + n / 16, and
-// cutting into chunks adds at most the number aimed at; parts come from all of them in groups, else only
-// from jobs that are cut.
+// Bounds for one layer.  Shares: the workgroups aimed at, and one.  Streamed pieces: one for each share and one
+// more for each stream.  An item job of n > 16 columns has 8 ceil(n / 128) items a chunk, at most n / 2
+// (8 at 17, 16 at 129) and 8 + n / 16; the items of jobs cut into more chunks and the shares are together
+// at most the workgroups aimed at, and one.  Parts come from all items in groups, else only from jobs
+// that are cut.
 struct Sizes {
-  int32_t stream_wgs, tile_items, items, unit_cols, stream_units, max_units;
-  size_t flags, desc, ml, acc, total;
+  int32_t wgs, both_wgs, grid, unit_cols, stream_units, max_units;
+  size_t desc, ml, acc, total;
 };
 
 Sizes sizes_of(int64_t L, int64_t B, int64_t n_groups, int64_t n_q, int64_t G) {
   Sizes z;
   const bool grouped = n_groups < B;
-  const int64_t cols = n_q * G;
+  const int64_t cols = n_q * G, all_cols = cols * (grouped ? 2 : 1);
   auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
-  z.stream_wgs = (int32_t)(L < kStreamWgs ? kStreamWgs / L : 1);
+  z.wgs = (int32_t)(L < kWgs ? kWgs / L : 1);
+  z.both_wgs = z.wgs > kBothWgs ? z.wgs : kBothWgs;
   // every sequence with tokens, and the shared rows of two or more of a group or behind one on its own
   const int64_t jobs = least(B, n_q) + (grouped ? least(n_groups + cols / kAlone, least(B, n_q)) : 0);
-  z.stream_units = (int32_t)(kWaves * (z.stream_wgs + kSets * jobs));
-  z.tile_items = z.items = 0;
-  int64_t parts = 0;
-  if (cols > kStreamCols) {
-    z.tile_items = (int32_t)(L < kTileItems ? kTileItems / L : 1);
-    const int64_t all_cols = cols * (grouped ? 2 : 1);
-    const int64_t items = z.tile_items + least(all_cols / 2, kHeads * jobs + all_cols / 16);
-    z.items = (int32_t)items;
-    parts = grouped ? items : least(items, 2 * z.tile_items);
-  }
+  const int64_t aimed = (cols > kStreamCols ? z.both_wgs : z.wgs) + 1;
+  const int64_t whole = cols > kStreamCols ? least(all_cols / 2, kHeads * jobs + all_cols / 16) : 0;
+  z.grid = (int32_t)(aimed + whole);
   z.unit_cols = (int32_t)least(cols, kCols);
-  z.max_units = (int32_t)(z.stream_units + kWaves * parts);
+  z.stream_units = (int32_t)(kWaves * (aimed + kSets * jobs));
+  z.max_units = (int32_t)(z.stream_units + (cols > kStreamCols ? kWaves * (aimed + (grouped ? whole : 0)) : 0));
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  z.flags = up((size_t)L * sizeof(int32_t));
   z.desc = up((size_t)L * n_q * 4 * sizeof(int4));
   z.ml = up((size_t)L * z.max_units * z.unit_cols * sizeof(float2));
   z.acc = up((size_t)L * z.max_units * z.unit_cols * kDim * sizeof(float));
-  z.total = z.flags + z.desc + z.ml + z.acc;
+  z.total = z.desc + z.ml + z.acc;
   return z;
 }
 
@@ -1243,9 +1265,7 @@ size_t attend_workspace_bytes(int32_t L, int32_t B, int32_t n_groups, int32_t n_
 
 template <bool BF16_OUT>
 static void launch_attend_as(const AttendArgs& a, const Sizes& z, int32_t L, hipStream_t s) {
-  hipLaunchKernelGGL(attend_stream_kernel<BF16_OUT>, dim3((unsigned)z.stream_wgs, (unsigned)L), dim3(kThreads), 0, s, a);
-  if (z.items > 0)
-    hipLaunchKernelGGL(attend_tile_kernel<BF16_OUT>, dim3((unsigned)z.items, (unsigned)L), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL(attend_kernel<BF16_OUT>, dim3((unsigned)z.grid, (unsigned)L), dim3(kThreads), 0, s, a);
   // a workgroup for 8 heads of one token, of several (at most 64) where there are many
   const int64_t rows = (int64_t)a.n_q * a.G * L;
   const int32_t per = (int32_t)(rows < 8192 ? 1 : (rows > 64 * 8192 ? 64 : rows / 8192));
@@ -1263,10 +1283,9 @@ hipError_t launch_attend(int32_t L, int32_t B, int32_t n_groups, int32_t n_q, in
   char* w = static_cast<char*>(ws);
   const AttendArgs a = {B, n_groups, n_q, Hq, Hq / kHeads, __builtin_ctz(Hq / kHeads), max_ctx, n_pages, page_shift, max_pages, q, q_off, grp_off,
                         ctx_k, ctx_v, ctx_len, k_pages, v_pages, page_table, kv_len, pre_len,
-                        scale * 1.4426950408889634f, out, z.stream_wgs, z.tile_items, z.unit_cols, z.stream_units,
-                        z.max_units, reinterpret_cast<uint32_t*>(w), reinterpret_cast<int4*>(w + z.flags),
-                        reinterpret_cast<float2*>(w + z.flags + z.desc),
-                        reinterpret_cast<float*>(w + z.flags + z.desc + z.ml)};
+                        scale * 1.4426950408889634f, out, z.wgs, z.both_wgs, z.unit_cols, z.stream_units, z.max_units,
+                        reinterpret_cast<int4*>(w), reinterpret_cast<float2*>(w + z.desc),
+                        reinterpret_cast<float*>(w + z.desc + z.ml)};
   if (bf16_out) launch_attend_as<true>(a, z, L, s);
   else launch_attend_as<false>(a, z, L, s);
   return hipGetLastError();
