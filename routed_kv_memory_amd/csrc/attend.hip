@@ -83,7 +83,7 @@ struct Job {
   int32_t shared, split;   // the group's shared rows; own rows next to a shared job
 };
 
-// The lengths of one layer, clamped, in LDS (in the memory of the tiles, before those come).
+// The lengths of one layer in LDS (in the memory of the tiles, before those come), clamped but for kv_len.
 struct Lengths {
   int32_t *off, *grp;             // [kMaxSeqs + 1]
   int32_t *len, *clen, *pre;      // [kMaxSeqs]
@@ -124,7 +124,7 @@ __device__ __forceinline__ void load_lengths(const AttendArgs& a, const Lengths&
   const int32_t cap = a.max_pages << a.page_shift;
   for (int32_t i = tid; i <= a.B; i += kThreads) {
     n.off[i] = clampi(a.q_off[i], 0, a.n_q);
-    if (i < a.B) n.len[i] = clampi(a.kv_len[i], 0, cap);
+    if (i < a.B) n.len[i] = a.kv_len[i];
   }
   for (int32_t g = tid; g <= a.n_groups; g += kThreads) {
     if (grouped) n.grp[g] = clampi(a.grp_off[g], 0, a.B);
@@ -161,7 +161,7 @@ __device__ __forceinline__ int32_t group_of(const AttendArgs& a, const Lengths& 
 __device__ __forceinline__ Job job_of(const AttendArgs& a, const Lengths& n, int32_t j) {
   const bool grouped = a.grp_off != nullptr;
   Job x;
-  const int32_t b = j < a.B ? j : j - a.B;
+  const int32_t b = j < a.B ? j : j - a.B, cap = a.max_pages << a.page_shift;
   x.shared = j >= a.B;
   x.t0 = n.off[b];
   x.cols = 0;
@@ -172,7 +172,7 @@ __device__ __forceinline__ Job job_of(const AttendArgs& a, const Lengths& n, int
     x.cols = max(0, n.off[b + 1] - x.t0) * a.G;
     x.grp = b;
     x.c = n.clen[b];
-    x.p1 = n.len[b];
+    x.p1 = clampi(n.len[b], 0, cap);
     return x;
   }
   const bool first = starts(n, b), alone = first && starts(n, b + 1);
@@ -193,7 +193,7 @@ __device__ __forceinline__ Job job_of(const AttendArgs& a, const Lengths& n, int
     return x;
   }
   x.cols = max(0, n.off[b + 1] - x.t0) * a.G;
-  x.p1 = n.len[b];
+  x.p1 = clampi(n.len[b], 0, cap);
   if (!alone) {
     x.split = x.c + pre > 0;
     x.c = 0;
@@ -207,6 +207,14 @@ __device__ __forceinline__ Job job_of(const AttendArgs& a, const Lengths& n, int
 __device__ __forceinline__ int32_t ctx_tiles(const Job& x, int32_t t) { return (x.c + t - 1) / t; }
 __device__ __forceinline__ int32_t tiles_of(const Job& x, int32_t t) {
   return max(1, ctx_tiles(x, t) + (max(0, x.p1 - x.p0) + t - 1) / t);
+}
+
+// Keeps a uniform value in scalar registers: the compiler would rather load kernel arguments again in every
+// tile, and wait for them.
+template <typename T>
+__device__ __forceinline__ T kept(T v) {
+  asm("" : "+s"(v));
+  return v;
 }
 
 // Row of the page pool of job row lr (a local row).
@@ -503,8 +511,8 @@ __device__ __forceinline__ void describe(const AttendArgs& a, const Job& x, cons
 //
 // The other jobs make items: a column block of 128, one head, a chunk of the rows.  A job's rows are cut
 // into its share of the workgroups, rounded down, so that they all run at once, but into chunks of
-// eight tiles at least.  The items come first (workgroups start in order), and of a job those of the last
-// column blocks, whose tokens see the most rows; heads fastest (workgroups go to the 8 XCDs in turn: a
+// eight tiles at least.  Of a job's items those of the last column blocks, whose tokens see the most rows,
+// come first (workgroups start in order); heads fastest (workgroups go to the 8 XCDs in turn: a
 // head's rows stay in one L2).
 
 __device__ __forceinline__ bool streamed(const Job& x) { return x.cols <= kStreamCols; }
@@ -518,6 +526,7 @@ __device__ __forceinline__ int32_t items_of(const Job& x) { return (x.cols + kWi
 
 struct Plan {
   int32_t j0, j1;                 // this thread's jobs
+  Job first;                      // the first of them (mostly the only one)
   uint32_t tiles, streams;        // of streamed jobs before them
   uint32_t items, units;          // items, and those that are parts, before them
   uint32_t all_tiles, all_items, share, shares;    // tiles of a share, shares
@@ -529,12 +538,14 @@ __device__ __forceinline__ Plan make_plan(const AttendArgs& a, const Lengths& n,
   const int32_t nj = a.grp_off ? 2 * a.B : a.B, per = (nj + kThreads - 1) / kThreads;
   p.j0 = min(nj, tid * per);
   p.j1 = min(nj, p.j0 + per);
+  p.first.cols = 0;
+  if (p.j0 < p.j1) p.first = job_of(a, n, p.j0);
   // tiles of a layer's streams fit 32 bits: 2 x 4,096 streams of at most 2 x 2^17 tiles.  Work of the
   // items: fp32 sum of whole numbers, in the same order in every workgroup
   uint32_t tiles = 0, streams = 0, all[2];
   float work = 0.f;
   for (int32_t j = p.j0; j < p.j1; ++j) {
-    const Job x = job_of(a, n, j);
+    const Job x = j == p.j0 ? p.first : job_of(a, n, j);
     if (x.cols == 0) continue;
     if (streamed(x)) {
       tiles += kSets * tiles_of(x, kStreamRows);
@@ -559,14 +570,15 @@ __device__ __forceinline__ Plan make_plan(const AttendArgs& a, const Lengths& n,
   p.aim = 0.f;
   p.shares = a.wgs;
   if (work > 0.f) {                               // uniform
-    // a streamed tile is 4 heads' rows, a shared one is one head's: both take their bytes' time, or as long
-    const float streams_work = 4.f * (float)p.all_tiles;
+    // a streamed tile is 4 heads' rows, an item's is one head's, of more columns: 4.2 against 1.2 us where
+    // both wait for HBM, 2.7 against 1.3 next to items bound by the matrix cores
+    const float streams_work = 3.f * (float)p.all_tiles;
     const int32_t wgs = p.all_tiles ? a.both_wgs : a.wgs;
     // 2^-10 below: the roundings of the sum
     p.aim = wgs * (1.f - 0x1p-10f) / (work + streams_work);
     uint32_t items = 0, units = 0;
     for (int32_t j = p.j0; j < p.j1; ++j) {
-      const Job x = job_of(a, n, j);
+      const Job x = j == p.j0 ? p.first : job_of(a, n, j);
       if (x.cols == 0 || streamed(x)) continue;
       const int32_t nch = chunks_of(x, p.aim);
       const uint32_t k = nch * items_of(x);
@@ -580,9 +592,9 @@ __device__ __forceinline__ Plan make_plan(const AttendArgs& a, const Lengths& n,
     p.units = units - p.units;
     p.all_items = all[0];
     p.shares = max((int32_t)(streams_work * p.aim), wgs - (int32_t)min(p.all_items, (uint32_t)wgs));
-    p.shares = max(p.shares, 1u);
+    p.shares = p.all_tiles ? max(p.shares, 1u) : 0u;
   }
-  p.share = max(1u, (p.all_tiles + p.shares - 1) / p.shares);
+  p.share = p.shares ? max(1u, (p.all_tiles + p.shares - 1) / p.shares) : 1u;
   return p;
 }
 
@@ -608,7 +620,7 @@ __device__ __forceinline__ uint32_t list_segments(const AttendArgs& a, const Len
   auto walk = [&](auto&& f) __attribute__((always_inline)) {
     uint32_t u = p.tiles, s = p.streams;
     for (int32_t j = p.j0; j < p.j1 && u < to; ++j) {
-      const Job x = job_of(a, n, j);
+      const Job x = j == p.j0 ? p.first : job_of(a, n, j);
       if (x.cols == 0 || !streamed(x)) continue;
       const uint32_t t = tiles_of(x, kStreamRows);
       for (int set = 0; set < kSets; ++set, u += t, ++s)
@@ -630,7 +642,7 @@ __device__ __forceinline__ uint32_t list_segments(const AttendArgs& a, const Len
     g.tile0 = (int32_t)(max(from, u) - u);
     g.tile1 = (int32_t)(min(to, u + t) - u);
     g.first = set == 0 && g.tile0 == 0;
-    g.limit0 = visible_rows(n.len[x.seq] > 0 ? a.kv_len[x.seq] : 0, n.off[x.seq + 1], x.t0) - x.p0;
+    g.limit0 = visible_rows(n.len[x.seq], n.off[x.seq + 1], x.t0) - x.p0;
     // the stream's tiles lie in shares w0 .. w1; stream + share number is a number of its own for every
     // piece, consecutive along a stream
     bool whole = true;
@@ -665,7 +677,7 @@ __device__ __forceinline__ void find_item(const AttendArgs& a, const Lengths& n,
   __syncthreads();
   uint32_t at = p.items, u = p.units;
   for (int32_t j = p.j0; j < p.j1 && at <= id; ++j) {
-    const Job x = job_of(a, n, j);
+    const Job x = j == p.j0 ? p.first : job_of(a, n, j);
     if (x.cols == 0 || streamed(x)) continue;
     const int32_t nch = chunks_of(x, p.aim), ncb = items_of(x) / kHeads;
     const uint32_t k = nch * ncb * kHeads;
@@ -746,6 +758,10 @@ __device__ __forceinline__ void attend_streams(const AttendArgs& a, const Length
   const int j = lane & 15, g = lane >> 4;
   auto uni = [](int32_t v) { return __builtin_amdgcn_readfirstlane(v); };
 
+  const uint16_t *ctx_k = kept(a.ctx_k), *ctx_v = kept(a.ctx_v), *page_k = kept(a.k_pages), *page_v = kept(a.v_pages);
+  const int32_t max_ctx = kept(a.max_ctx);
+  const int64_t ctx_row = kept(layer * a.n_groups * (int64_t)a.max_ctx), page_row0 = kept((layer * a.n_pages) << a.page_shift);
+
   for (uint32_t from = 0;;) {
     if (tid < 3) n_seg[tid] = 0;
     __syncthreads();
@@ -783,10 +799,9 @@ __device__ __forceinline__ void attend_streams(const AttendArgs& a, const Length
     u32x4 pk[8], pv[8];
     auto load = [&](const Cursor& u, int32_t where) __attribute__((always_inline)) {
       const bool ctx = u.tile < u.nctx;
-      const int64_t base = (ctx ? (layer * a.n_groups + u.grp) * (int64_t)a.max_ctx : (layer * a.n_pages) << a.page_shift) *
-                               kRow + u.head * kDim;
-      const uint16_t* kb = (ctx ? a.ctx_k : a.k_pages) + base;
-      const uint16_t* vb = (ctx ? a.ctx_v : a.v_pages) + base;
+      const int64_t base = (ctx ? (ctx_row + u.grp * (int64_t)max_ctx) : page_row0) * kRow + u.head * kDim;
+      const uint16_t* kb = (ctx ? ctx_k : page_k) + base;
+      const uint16_t* vb = (ctx ? ctx_v : page_v) + base;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int64_t off = (int64_t)__shfl(where, 4 * i + g, 64) * kRow + 8 * j;
@@ -976,7 +991,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
   int32_t limit = 0;                                 // first local row (from p0) the column does not see
   if (y.live && x.p1 > x.p0) {
     const int32_t b = x.shared ? min(count_upto(n.off, a.B, y.t), a.B - 1) : x.seq;
-    limit = clampi(visible_rows(a.kv_len[b], n.off[b + 1], y.t) - x.p0, 0, x.p1 - x.p0);
+    limit = clampi(visible_rows(n.len[b], n.off[b + 1], y.t) - x.p0, 0, x.p1 - x.p0);
   }
   int32_t most = limit, least = y.live ? limit : 0x7FFFFFFF;
 #pragma unroll
@@ -1004,29 +1019,57 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
   wg_most = uni(wg_most);
   tile1 = min(tile1, nctx + (wg_most + kTileRows - 1) / kTileRows);
 
-  // this wave's loads: rows 8 wave + 4 i + (lane >> 4) of K and of V
+  // This wave's loads: rows 8 wave + 4 i + (lane >> 4) of K and of V.  The tiles' rows are found by waves: 8
+  // memory rows follow each other, and so do 8 local rows of a page, so one row number and fixed lane offsets address a wave's loads of a whole tile.  Partial
+  // tiles, and local rows that do not lie in eights (small pages, an odd start), are found row by row.
   constexpr int kPer = kTileRows / 4 / kWaves;
-  const int lr = 4 * kPer * wave + (lane >> 4);
   const int64_t ctx_at = (layer * a.n_groups + uni(x.grp)) * (int64_t)a.max_ctx * kRow + head * kDim;
   const int64_t page_at = ((layer * a.n_pages) << a.page_shift) * kRow + head * kDim;
-  int32_t where[kPer];
-  auto find = [&](int32_t t) __attribute__((always_inline)) {
+  const uint16_t *ctx_k = kept(a.ctx_k + ctx_at), *ctx_v = kept(a.ctx_v + ctx_at);
+  const uint16_t *page_k = kept(a.k_pages + page_at), *page_v = kept(a.v_pages + page_at);
+  const auto* table = (const __attribute__((address_space(4))) int32_t*)kept(a.page_table + (int64_t)seq * a.max_pages);
+  const int32_t shift = kept(a.page_shift), last_page = kept(a.n_pages - 1);
+  const int w8 = uni(4 * kPer * wave);
+  const bool eights = shift >= 3 && (p0 & 7) == 0;
+  uint32_t k_lane[kPer], v_lane[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (t < nctx) where[i] = min(t * kTileRows + 4 * i + lr, jc - 1);
-      else where[i] = page_row(a, seq, p0 + min((t - nctx) * kTileRows + 4 * i + lr, wg_most - 1));
-    }
+  for (int i = 0; i < kPer; ++i) {
+    const int r = 4 * i + (lane >> 4);
+    k_lane[i] = r * kRow + 8 * ((lane & 15) ^ ((w8 + r) & 15));
+    v_lane[i] = r * kRow + 8 * ((lane & 15) ^ (4 * (lane >> 4)));
+  }
+  // the page of the wave's rows of a page tile, as it stands in the table: a scalar load (a vector load's result
+  // would only come after all the tile loads issued before it), not waited for before the tile's turn
+  int32_t page = 0;
+  auto local_row = [&](int32_t t) __attribute__((always_inline)) {
+    return p0 + min((t - nctx) * kTileRows + w8, wg_most - 1);
+  };
+  auto find = [&](int32_t t) __attribute__((always_inline)) {
+    if (t >= nctx) page = table[local_row(t) >> shift];
   };
   auto issue = [&](int32_t t, u32x4* stage) __attribute__((always_inline)) {
-    const uint16_t* kb = t < nctx ? a.ctx_k + ctx_at : a.k_pages + page_at;
-    const uint16_t* vb = t < nctx ? a.ctx_v + ctx_at : a.v_pages + page_at;
+    const bool ctx = t < nctx;
+    const uint16_t *kb = ctx ? ctx_k : page_k, *vb = ctx ? ctx_v : page_v;
+    u32x4* to = stage + kPer * wave * 64;
+    if (ctx ? (t + 1) * kTileRows <= jc : eights && (t - nctx + 1) * kTileRows <= wg_most) {
+      int32_t row = t * kTileRows + w8;
+      if (!ctx) row = (clampi(page, 0, last_page) << shift) + (local_row(t) & ((1 << shift) - 1));
+      const int64_t at = (int64_t)row * kRow;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int64_t row = (int64_t)where[i] * kRow;
-      const int ck = (lane & 15) ^ ((4 * i + lr) & 15), cv = (lane & 15) ^ (4 * (lane >> 4));
-      u32x4* to = stage + (kPer * wave + i) * 64;
-      __builtin_amdgcn_global_load_lds((gptr_t)(kb + row + 8 * ck), (lptr_t)to, 16, 0, 0);
-      __builtin_amdgcn_global_load_lds((gptr_t)(vb + row + 8 * cv), (lptr_t)(to + kTileRows * 16), 16, 0, 0);
+      for (int i = 0; i < kPer; ++i) {
+        __builtin_amdgcn_global_load_lds((gptr_t)(kb + at + k_lane[i]), (lptr_t)(to + 64 * i), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((gptr_t)(vb + at + v_lane[i]), (lptr_t)(to + 64 * i + kTileRows * 16), 16, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int r = 4 * i + (lane >> 4);
+        const int32_t row = ctx ? min(t * kTileRows + w8 + r, jc - 1)
+                                : page_row(a, seq, p0 + min((t - nctx) * kTileRows + w8 + r, wg_most - 1));
+        const int64_t at = (int64_t)(row - r) * kRow;
+        __builtin_amdgcn_global_load_lds((gptr_t)(kb + at + k_lane[i]), (lptr_t)(to + 64 * i), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((gptr_t)(vb + at + v_lane[i]), (lptr_t)(to + 64 * i + kTileRows * 16), 16, 0, 0);
+      }
     }
   };
   const StageReads at(lane);
@@ -1133,19 +1176,23 @@ attend_kernel(const AttendArgs a) {
     } streams;
   } sh;
   const int tid = threadIdx.x;
-  const int64_t layer = blockIdx.y;
+  // layers fastest: the workgroups that turn out to have nothing to do come last
+  const int64_t layer = blockIdx.x;
   const Lengths n = lengths_in(stage0, stage1, stage2, stage3);
   load_lengths(a, n, layer, tid);
   const Plan p = make_plan(a, n, tid);
-  const uint32_t id = blockIdx.x;
-  if (id < p.all_items) {                         // uniform
-    find_item(a, n, p, sh.item.item, id, tid);
-    if (sh.item.item.valid) attend_item<BF16_OUT>(a, n, sh.item, stage0, stage1, stage2, stage3, layer, tid);
-  } else if (id - p.all_items < p.shares) {
+  const uint32_t id = blockIdx.y;
+  // items that fit the chip at once are the longer ones; items of many rounds end more evenly than shares
+  const bool items_first = p.all_items <= (uint32_t)a.both_wgs;
+  const uint32_t first_share = items_first ? p.all_items : 0, first_item = items_first ? 0 : p.shares;
+  if (id >= first_share && id < first_share + p.shares) {      // uniform
     const int wave = tid >> 6;
     u32x4* tile = wave == 0 ? stage0 : (wave == 1 ? stage1 : (wave == 2 ? stage2 : stage3));
-    attend_streams<BF16_OUT>(a, n, p, sh.streams.seg, sh.streams.n_seg, reinterpret_cast<uint16_t*>(tile), id - p.all_items,
-                             layer, tid);
+    attend_streams<BF16_OUT>(a, n, p, sh.streams.seg, sh.streams.n_seg, reinterpret_cast<uint16_t*>(tile),
+                             id - first_share, layer, tid);
+  } else if (id >= first_item && id < first_item + p.all_items) {
+    find_item(a, n, p, sh.item.item, id - first_item, tid);
+    if (sh.item.item.valid) attend_item<BF16_OUT>(a, n, sh.item, stage0, stage1, stage2, stage3, layer, tid);
   }
 }
 
@@ -1224,7 +1271,7 @@ attend_join_kernel(const AttendArgs a, int32_t per) {
   }
 }
 
-// Bounds for one layer.  Shares: the workgroups aimed at, and one.  Streamed pieces: one for each share and one
+// Bounds for one layer.  Shares: the workgroups aimed at, one more next to items.  Streamed pieces: one for each share and one
 // more for each stream.  An item job of n > 16 columns has 8 ceil(n / 128) items a chunk, at most n / 2
 // (8 at 17, 16 at 129) and 8 + n / 16; the items of jobs cut into more chunks and the shares are together
 // at most the workgroups aimed at, and one.  Parts come from all items in groups, else only from jobs
@@ -1243,7 +1290,7 @@ Sizes sizes_of(int64_t L, int64_t B, int64_t n_groups, int64_t n_q, int64_t G) {
   z.both_wgs = z.wgs > kBothWgs ? z.wgs : kBothWgs;
   // every sequence with tokens, and the shared rows of two or more of a group or behind one on its own
   const int64_t jobs = least(B, n_q) + (grouped ? least(n_groups + cols / kAlone, least(B, n_q)) : 0);
-  const int64_t aimed = (cols > kStreamCols ? z.both_wgs : z.wgs) + 1;
+  const int64_t aimed = cols > kStreamCols ? z.both_wgs + 1 : z.wgs;
   const int64_t whole = cols > kStreamCols ? least(all_cols / 2, kHeads * jobs + all_cols / 16) : 0;
   z.grid = (int32_t)(aimed + whole);
   z.unit_cols = (int32_t)least(cols, kCols);
@@ -1265,7 +1312,7 @@ size_t attend_workspace_bytes(int32_t L, int32_t B, int32_t n_groups, int32_t n_
 
 template <bool BF16_OUT>
 static void launch_attend_as(const AttendArgs& a, const Sizes& z, int32_t L, hipStream_t s) {
-  hipLaunchKernelGGL(attend_kernel<BF16_OUT>, dim3((unsigned)z.grid, (unsigned)L), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL(attend_kernel<BF16_OUT>, dim3((unsigned)L, (unsigned)z.grid), dim3(kThreads), 0, s, a);
   // a workgroup for 8 heads of one token, of several (at most 64) where there are many
   const int64_t rows = (int64_t)a.n_q * a.G * L;
   const int32_t per = (int32_t)(rows < 8192 ? 1 : (rows > 64 * 8192 ? 64 : rows / 8192));
