@@ -910,7 +910,6 @@ __device__ __forceinline__ void attend_streams(const AttendArgs& a, const Length
 // once: chunk x of K row r lies at x ^ (r & 15) (16 rows, one chunk each), of V row r at
 // x ^ 4 (r & 3) (4 rows, 4 chunks each).
 static_assert(kStage == 2 * kTileRows * 16, "K rows and V rows");
-constexpr int kStages = 4;
 
 typedef __attribute__((address_space(1))) const void* gptr_t;
 typedef __attribute__((address_space(3))) void* lptr_t;
@@ -932,38 +931,49 @@ struct StageReads {
   }
 };
 
-// A stage's rows into the state; a column sees the first `left` of them (whole: all do).
-template <int PARTS, bool CAREFUL>
-__device__ __forceinline__ void attend_stage(const u32x4* stage, const StageReads& at, const u32x4* qf, bool whole,
-                                             int32_t left, float scale2, int h, State& st) {
-  f32x16 s = zeros16();
+// The rows of N stages into the state; a column sees the first left[u] of each (whole: all of all).  Two at once
+// make one decision about the maximum for 64 rows, and the second tile's scores are formed while the
+// first one's settle.
+template <int PARTS, bool CAREFUL, int N>
+__device__ __forceinline__ void attend_tiles(const u32x4* stage_a, const u32x4* stage_b, const StageReads& at, const u32x4* qf,
+                                             bool whole, int32_t left_a, int32_t left_b, float scale2, int h, State& st) {
+  f32x16 s[N];
 #pragma unroll
-  for (int d = 0; d < 8; ++d) s = mfma32(at.k(stage, d), qf[d], s);
+  for (int u = 0; u < N; ++u) {
+    s[u] = zeros16();
+#pragma unroll
+    for (int d = 0; d < 8; ++d) s[u] = mfma32(at.k(u ? stage_b : stage_a, d), qf[d], s[u]);
+  }
   u32x4 vf[2][4];               // on their way while the softmax runs
   if (!CAREFUL) {
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int d = 0; d < 4; ++d) vf[m][d] = at.v(stage, m, d);
+      for (int d = 0; d < 4; ++d) vf[m][d] = at.v(stage_a, m, d);
   }
   if (!whole) {
     asm volatile("" ::: );      // a branch: most tiles are whole, and selects for all would cost what the exps do
-    mask_rows(s, left, h);
+    mask_rows(s[0], left_a, h);
+    if (N == 2) mask_rows(s[N - 1], left_b, h);
   }
-  raise_to(halves_max(max16(s)), scale2, st);
+  float top = max16(s[0]);
+  if (N == 2) top = fmaxf(top, max16(s[N - 1]));
+  raise_to(halves_max(top), scale2, st);
   const float neg_m = st.m == -__builtin_huge_valf() ? 0.f : -st.m;
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    // k slot 8 h + e holds row 16 m + 4 h + e (e < 4) or 16 m + 8 + 4 h + e - 4
-    float v[8];
+  for (int u = 0; u < N; ++u)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = s[8 * m + e];
-    u32x4 ph, pl;
-    weights<PARTS>(v, scale2, neg_m, ph, pl, st.l);
+    for (int m = 0; m < 2; ++m) {
+      // k slot 8 h + e holds row 16 m + 4 h + e (e < 4) or 16 m + 8 + 4 h + e - 4
+      float v[8];
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
-      add_values<PARTS, CAREFUL>(CAREFUL ? at.v(stage, m, d) : vf[m][d], ph, pl, st.o[d]);
-  }
+      for (int e = 0; e < 8; ++e) v[e] = s[u][8 * m + e];
+      u32x4 ph, pl;
+      weights<PARTS>(v, scale2, neg_m, ph, pl, st.l);
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        add_values<PARTS, CAREFUL>(CAREFUL || u ? at.v(u ? stage_b : stage_a, m, d) : vf[m][d], ph, pl, st.o[d]);
+    }
 }
 
 struct ItemShared {
@@ -1040,14 +1050,15 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
   }
   // the page of the wave's rows of a page tile, as it stands in the table: a scalar load (a vector load's result
   // would only come after all the tile loads issued before it), not waited for before the tile's turn
-  int32_t page = 0;
+  int32_t page_a = 0, page_b = 0;
+  constexpr int kWaitOld = (4 * kPer) | 0x70, kWaitAll = 0x70;       // vmcnt, lgkmcnt 0
   auto local_row = [&](int32_t t) __attribute__((always_inline)) {
     return p0 + min((t - nctx) * kTileRows + w8, wg_most - 1);
   };
-  auto find = [&](int32_t t) __attribute__((always_inline)) {
+  auto find = [&](int32_t t, int32_t& page) __attribute__((always_inline)) {
     if (t >= nctx) page = table[local_row(t) >> shift];
   };
-  auto issue = [&](int32_t t, u32x4* stage) __attribute__((always_inline)) {
+  auto issue = [&](int32_t t, int32_t page, u32x4* stage) __attribute__((always_inline)) {
     const bool ctx = t < nctx;
     const uint16_t *kb = ctx ? ctx_k : page_k, *vb = ctx ? ctx_v : page_v;
     u32x4* to = stage + kPer * wave * 64;
@@ -1082,51 +1093,69 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
   auto whole = [&](int32_t t) __attribute__((always_inline)) {
     return (t < nctx ? jc - t * kTileRows : min(wg_most, least) - (t - nctx) * kTileRows) >= kTileRows;
   };
-  // One tile: this wave's loads of it have landed (they were issued three tiles ago; the loads of the two
-  // tiles after it may be in flight: 2 x 2 kPer), barrier (the tile is whole, and every wave is done with the
-  // tile before), load the tile three ahead into that one's stage, use this one.
-  constexpr int kWaitOld = (4 * kPer) | 0x70, kWaitAll = 0x70;       // vmcnt, lgkmcnt 0
-  auto step = [&](int32_t t, const u32x4* stage, u32x4* before, auto all_waves) __attribute__((always_inline)) {
+  const int32_t last = tile1 - 1;
+  // Four column blocks, bound by the matrix cores and the vector work: one tile a step.  This wave's loads of it
+  // have landed (they were issued three tiles ago; those of the two tiles after it may be in flight: 2 x 2 kPer),
+  // barrier (the tile is whole, and every wave is done with the tile before), load the tile three ahead into
+  // that one's stage, use this one.
+  auto step = [&](int32_t t, const u32x4* stage, u32x4* before) __attribute__((always_inline)) {
     if (t + 2 < tile1) __builtin_amdgcn_s_waitcnt(kWaitOld);
     else __builtin_amdgcn_s_waitcnt(kWaitAll);
     asm volatile("s_barrier" ::: "memory");
-    if (t + 3 < tile1) issue(t + 3, before);
-    if (t + 4 < tile1) find(t + 4);
-    if (all_waves || (t & (share - 1)) == turn)
-      attend_stage<PARTS, false>(stage, at, qf, whole(t), left_of(t), a.scale2, h, st);
-  };
-  auto run = [&](auto all_waves) __attribute__((always_inline)) {
-    for (int32_t t = tile0; t < tile1; t += kStages) {
-      step(t, stage0, stage3, all_waves);
-      if (t + 1 < tile1) step(t + 1, stage1, stage0, all_waves);
-      if (t + 2 < tile1) step(t + 2, stage2, stage1, all_waves);
-      if (t + 3 < tile1) step(t + 3, stage3, stage2, all_waves);
+    if (t + 3 < tile1) {
+      issue(t + 3, page_a, before);
+      find(min(t + 4, last), page_a);
     }
+    attend_tiles<PARTS, false, 1>(stage, stage, at, qf, whole(t), left_of(t), 0, a.scale2, h, st);
+  };
+  // Fewer blocks, bound by the rows' bytes: two tiles a step, for one of the block's waves.  An odd last tile comes
+  // with a copy of itself that nothing sees.
+  auto pair = [&](int32_t t, const u32x4* a0, const u32x4* a1, u32x4* b0, u32x4* b1) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(kWaitAll);
+    asm volatile("s_barrier" ::: "memory");
+    if (t + 2 < tile1) {
+      issue(t + 2, page_a, b0);
+      issue(min(t + 3, last), page_b, b1);
+      find(min(t + 4, last), page_a);
+      find(min(t + 5, last), page_b);
+    }
+    if (((t >> 1) & (share - 1)) == turn)
+      attend_tiles<PARTS, false, 2>(a0, a1, at, qf, t < last && whole(t) && whole(t + 1), left_of(t),
+                                    t < last ? left_of(t + 1) : 0, a.scale2, h, st);
   };
   if (tile0 < tile1) {
-    find(tile0);
-    issue(tile0, stage0);
-    if (tile0 + 1 < tile1) {
-      find(tile0 + 1);
-      issue(tile0 + 1, stage1);
+    find(tile0, page_a);
+    find(min(tile0 + 1, last), page_b);
+    issue(tile0, page_a, stage0);
+    issue(min(tile0 + 1, last), page_b, stage1);
+    find(min(tile0 + 2, last), page_a);
+    find(min(tile0 + 3, last), page_b);
+    if (blocks == kWaves) {
+      if (tile0 + 2 < tile1) issue(tile0 + 2, page_a, stage2);
+      page_a = page_b;
+      for (int32_t t = tile0; t < tile1; t += 4) {
+        step(t, stage0, stage3);
+        if (t + 1 < tile1) step(t + 1, stage1, stage0);
+        if (t + 2 < tile1) step(t + 2, stage2, stage1);
+        if (t + 3 < tile1) step(t + 3, stage3, stage2);
+      }
+    } else {
+      for (int32_t t = tile0; t < tile1; t += 4) {
+        pair(t, stage0, stage1, stage2, stage3);
+        if (t + 2 < tile1) pair(t + 2, stage2, stage3, stage0, stage1);
+      }
     }
-    if (tile0 + 2 < tile1) {
-      find(tile0 + 2);
-      issue(tile0 + 2, stage2);
-    }
-    if (tile0 + 3 < tile1) find(tile0 + 3);
-    if (blocks == kWaves) run(std::true_type());
-    else run(std::false_type());
   }
   if (__syncthreads_or(holds_nan(st))) {
     clear(st);
 #pragma unroll 1
     for (int32_t t = tile0; t < tile1; ++t) {
-      find(t);
-      issue(t, stage0);
+      find(t, page_a);
+      issue(t, page_a, stage0);
       __builtin_amdgcn_s_waitcnt(kWaitAll);
       __syncthreads();
-      if ((t & (share - 1)) == turn) attend_stage<PARTS, true>(stage0, at, qf, false, left_of(t), a.scale2, h, st);
+      if (((t >> 1) & (share - 1)) == turn)
+        attend_tiles<PARTS, true, 1>(stage0, stage0, at, qf, false, left_of(t), 0, a.scale2, h, st);
       __syncthreads();
     }
   }
