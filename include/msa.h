@@ -388,8 +388,9 @@ int msa_paged_append(int32_t n_layers, int32_t B, int32_t n_q, int32_t Hq, const
  * group g; new token i of sequence b of group g sees the group's memory rows 0 .. ctx_len[l][g])
  * and b's local rows 0 .. kv_len[b] - n + i (causal, as msa_sparse_prefill).  The memory rows,
  * and the first pre_len[g] local rows where that is given, are read once for all sequences of
- * the group: these local rows must lie in the same pages in all of them (the first sequence's
- * table is read).  One new token a sequence is the decode, many are the prefill; both may be
+ * the group (those with so many new tokens that this saves nothing read them themselves): these
+ * local rows must lie in the same pages in all of them (the first sequence's table is read).
+ * pre_len changes only what is read, not what a token sees.  One new token a sequence is the decode, many are the prefill; both may be
  * mixed in one call.
  *
  *   q             [n_layers][n_q][Hq][128] bf16, Hq in {8, 16, 32, 64}
@@ -403,8 +404,8 @@ int msa_paged_append(int32_t n_layers, int32_t B, int32_t n_q, int32_t Hq, const
  *                 a token that sees no row
  *
  * Scores, softmax and sums in fp32.  With fp32 output the probabilities enter the P.V product as
- * a bf16 high part plus a bf16 residual (~16 significant bits), with bf16 output as one bf16 value
- * (its rounding is the size of the output's own).  Rows a token does not see never reach its
+ * three bf16 parts (the fp32 value but for 2^-25 of it), with bf16 output as one bf16 value (its
+ * rounding is the size of the output's own).  Rows a token does not see never reach its
  * output, infinities and NaN in them included.  Lengths are clamped to [0, max_ctx] and
  * [0, max_pages * page_tokens], page numbers to [0, n_pages).  A workspace serves one call at a
  * time.  Errors: NULL pointers, sizes < 1, n_groups > B, Hq % 8 != 0, page_tokens no power of

@@ -338,7 +338,7 @@ __device__ __forceinline__ u32x4 without_specials(u32x4 raw, u32x4 bad, u32x4 p,
   return raw & ~bad;
 }
 
-// A masked row's weight is 0, but 0 * inf is NaN (and with probabilities in two parts, an infinity meets a
+// A masked row's weight is 0, but 0 * inf is NaN (and with probabilities in three parts, an infinity meets a
 // residual of either sign).  So when what was summed up holds NaN, it is gone through once more with
 // CAREFUL set, where V entries that are no finite numbers are taken out of the products: that gives
 // what the columns see and nothing else.
@@ -379,20 +379,28 @@ __device__ __forceinline__ void raise_to(float mt, float scale2, St& st) {
 }
 
 // Probabilities of 8 scores as a B operand of the second product, and into the sum.
-// PARTS: 2 gives a bf16 high part and a bf16 residual, 1 one bf16 value, whose rounding (2^-9 of each
-// weight) is the size of a bf16 output's own; the sum is then taken of the rounded values, so the
-// weights still add up to one.
+// PARTS 3 (fp32 output): three bf16 values, each the rounding of what those before it leave, together the fp32
+// value but for 2^-25 of it.  Two leave 2^-17: 2.3e-6 of the output against 4.3e-7 with three, for 850
+// against 985 us where the matrix cores bind (8 prompts of up to 1,088 tokens, 4 layers), next to nothing elsewhere.
+// PARTS 1 (bf16 output): one bf16 value, whose rounding (2^-8 of each weight) is the size of the
+// output's own; the sum is then taken of the rounded values, so the weights still add up to one.
 template <int PARTS>
-__device__ __forceinline__ void weights(const float* s, float scale2, float neg_m, u32x4& ph, u32x4& pl, float& l) {
+__device__ __forceinline__ void weights(const float* s, float scale2, float neg_m, u32x4* pw, float& l) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * e], scale2, neg_m));
     const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * e + 1], scale2, neg_m));
     const uint32_t w = pack2_bf16(p0, p1);
-    ph[e] = w;
-    if (PARTS == 2) {
-      pl[e] = pack2_bf16(p0 - __uint_as_float(w << 16), p1 - __uint_as_float(w & 0xFFFF0000u));
+    pw[0][e] = w;
+    if (PARTS > 1) {
       l += p0 + p1;
+      float r0 = p0 - __uint_as_float(w << 16), r1 = p1 - __uint_as_float(w & 0xFFFF0000u);
+      pw[1][e] = pack2_bf16(r0, r1);
+      if (PARTS > 2) {
+        r0 -= __uint_as_float(pw[1][e] << 16);
+        r1 -= __uint_as_float(pw[1][e] & 0xFFFF0000u);
+        pw[PARTS - 1][e] = pack2_bf16(r0, r1);
+      }
     } else {
       l = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), __builtin_bit_cast(bf16x2, 0x3F803F80u), l, false);
     }
@@ -401,15 +409,15 @@ __device__ __forceinline__ void weights(const float* s, float scale2, float neg_
 
 // O^T += V^T . P^T for one fragment of V^T.
 template <int PARTS, bool CAREFUL, typename Acc>
-__device__ __forceinline__ void add_values(u32x4 vf, const u32x4& ph, const u32x4& pl, Acc& o) {
+__device__ __forceinline__ void add_values(u32x4 vf, const u32x4* pw, Acc& o) {
   if (CAREFUL) {
     u32x4 bad;
 #pragma unroll
     for (int e = 0; e < 4; ++e) bad[e] = not_finite(vf[e]);
-    if (__ballot((bad[0] | bad[1] | bad[2] | bad[3]) != 0)) vf = without_specials(vf, bad, ph, o);
+    if (__ballot((bad[0] | bad[1] | bad[2] | bad[3]) != 0)) vf = without_specials(vf, bad, pw[0], o);
   }
-  o = mfma_of(vf, ph, o);
-  if (PARTS == 2) o = mfma_of(vf, pl, o);
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) o = mfma_of(vf, pw[i], o);
 }
 
 template <typename St>
@@ -737,13 +745,13 @@ __device__ __forceinline__ void attend_rows(uint16_t* tile, const u32x4* pv, con
     mt = fmaxf(mt, v[e]);
   }
   raise_to(rows4_max(mt), scale2, st);
-  u32x4 ph, pl;
-  weights<PARTS>(v, scale2, st.m == -__builtin_huge_valf() ? 0.f : -st.m, ph, pl, st.l);
+  u32x4 pw[PARTS];
+  weights<PARTS>(v, scale2, st.m == -__builtin_huge_valf() ? 0.f : -st.m, pw, st.l);
   // a 16-lane group reads 16 dims of 4 rows transposed
   const uint16_t* vsrc = tile + (4 * g + (j >> 2)) * kVStride + 4 * (j & 3);
 #pragma unroll
   for (int d = 0; d < 8; ++d)
-    add_values<PARTS, CAREFUL>(frag_of(lds_read_tr16(vsrc + 16 * d), lds_read_tr16(vsrc + 16 * kVStride + 16 * d)), ph, pl,
+    add_values<PARTS, CAREFUL>(frag_of(lds_read_tr16(vsrc + 16 * d), lds_read_tr16(vsrc + 16 * kVStride + 16 * d)), pw,
                                st.o[d]);
 }
 
@@ -751,7 +759,7 @@ __device__ __forceinline__ void attend_rows(uint16_t* tile, const u32x4* pv, con
 template <bool BF16_OUT>
 __device__ __forceinline__ void attend_streams(const AttendArgs& a, const Lengths& n, Plan p, Segment* seg, uint32_t* n_seg,
                                                uint16_t* tile, uint32_t number, int64_t layer, int tid) {
-  constexpr int PARTS = BF16_OUT ? 1 : 2;
+  constexpr int PARTS = BF16_OUT ? 1 : 3;
   static_assert(kStage * 16 >= kStreamRows * kVStride * 2, "a stage holds a wave's tile");
   const int lane = tid & 63, wave = tid >> 6;
   // rows by whole 16-lane groups: load i brings rows 4 i + g, dims 8 j .. 8 j + 7
@@ -968,11 +976,11 @@ __device__ __forceinline__ void attend_tiles(const u32x4* stage_a, const u32x4* 
       float v[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = s[u][8 * m + e];
-      u32x4 ph, pl;
-      weights<PARTS>(v, scale2, neg_m, ph, pl, st.l);
+      u32x4 pw[PARTS];
+      weights<PARTS>(v, scale2, neg_m, pw, st.l);
 #pragma unroll
       for (int d = 0; d < 4; ++d)
-        add_values<PARTS, CAREFUL>(CAREFUL || u ? at.v(u ? stage_b : stage_a, m, d) : vf[m][d], ph, pl, st.o[d]);
+        add_values<PARTS, CAREFUL>(CAREFUL || u ? at.v(u ? stage_b : stage_a, m, d) : vf[m][d], pw, st.o[d]);
     }
 }
 
@@ -986,7 +994,7 @@ struct ItemShared {
 template <bool BF16_OUT>
 __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& n, ItemShared& z, u32x4* stage0, u32x4* stage1,
                                             u32x4* stage2, u32x4* stage3, int64_t layer, int tid) {
-  constexpr int PARTS = BF16_OUT ? 1 : 2;
+  constexpr int PARTS = BF16_OUT ? 1 : 3;
   const int lane = tid & 63, wave = tid >> 6;
   const int c = lane & 31, h = lane >> 5;
   const Item& it = z.item;
@@ -1195,7 +1203,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
 
 template <bool BF16_OUT>
 __global__ void __launch_bounds__(kThreads, 2)
-attend_kernel(const AttendArgs a) {
+attend_kernel(const AttendArgs a, const uint32_t L) {
   __shared__ u32x4 stage0[kStage], stage1[kStage], stage2[kStage], stage3[kStage];
   __shared__ union {
     ItemShared item;
@@ -1206,11 +1214,11 @@ attend_kernel(const AttendArgs a) {
   } sh;
   const int tid = threadIdx.x;
   // layers fastest: the workgroups that turn out to have nothing to do come last
-  const int64_t layer = blockIdx.x;
+  const int64_t layer = blockIdx.x % L;
   const Lengths n = lengths_in(stage0, stage1, stage2, stage3);
   load_lengths(a, n, layer, tid);
   const Plan p = make_plan(a, n, tid);
-  const uint32_t id = blockIdx.y;
+  const uint32_t id = blockIdx.x / L;
   // items that fit the chip at once are the longer ones; items of many rounds end more evenly than shares
   const bool items_first = p.all_items <= (uint32_t)a.both_wgs;
   const uint32_t first_share = items_first ? p.all_items : 0, first_item = items_first ? 0 : p.shares;
@@ -1341,7 +1349,7 @@ size_t attend_workspace_bytes(int32_t L, int32_t B, int32_t n_groups, int32_t n_
 
 template <bool BF16_OUT>
 static void launch_attend_as(const AttendArgs& a, const Sizes& z, int32_t L, hipStream_t s) {
-  hipLaunchKernelGGL(attend_kernel<BF16_OUT>, dim3((unsigned)L, (unsigned)z.grid), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL(attend_kernel<BF16_OUT>, dim3((unsigned)(L * (int64_t)z.grid)), dim3(kThreads), 0, s, a, (uint32_t)L);
   // a workgroup for 8 heads of one token, of several (at most 64) where there are many
   const int64_t rows = (int64_t)a.n_q * a.G * L;
   const int32_t per = (int32_t)(rows < 8192 ? 1 : (rows > 64 * 8192 ? 64 : rows / 8192));
