@@ -296,11 +296,8 @@ def msa_encode_blocks(x, w_k, w_v, w_kr, w_norm, eps, theta, doc_tok_off, doc_bl
 _F32_BF16 = (torch.float32,) + _BF16
 
 
-def _shape(t, shape, name):
-    """An optional tensor of exactly this shape (the kernels take the sizes from other arguments)."""
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-
+# A decode step makes these calls with a dozen tensors around kernels of a few microseconds: each tensor is
+# looked at once, and neither a stream object nor a device guard is made where the device is the current one.
 
 def _dims(t, n, name):
     """The sizes of a required n-dimensional tensor."""
@@ -311,28 +308,49 @@ def _dims(t, n, name):
     return t.shape
 
 
-def _one_device(stream, first, *rest):
-    """The device of the tensors (the kernels run on it) and the stream as a pointer."""
-    dev = first.device
-    for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError("tensors on %s and %s" % (dev, t.device))
+def _on(dev, t, dtypes, shape, name):
+    """Address of a contiguous tensor of this shape on GPU `dev` (the kernels take the sizes from other
+    arguments); None for none."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.dtype not in dtypes:
+        raise TypeError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtypes))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    d = t.get_device()
+    if d != dev or d < 0:
+        if not t.is_cuda:
+            raise ValueError("%s must be a GPU tensor" % name)
+        raise ValueError("%s is on cuda:%d, the other tensors on cuda:%d" % (name, d, dev))
+    return t.data_ptr()
+
+
+def _required(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError("%s is required" % name)
+
+
+def _call(fn, dev, stream, args):
+    """The entry point on the tensors' device, on `stream` or that device's current one."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError("stream on %s, tensors on %s" % (stream.device, dev))
-    return dev, ctypes.c_void_p(stream.cuda_stream)
-
-
-def _paged(k_pages, v_pages, page_table, q_off, kv_len, L):
-    """Sizes (n_pages, page_tokens, B, max_pages) of a paged cache, its arrays checked against them."""
-    Lp, n_pages, page_tokens, h, d = _dims(k_pages, 5, "k_pages")
-    B, max_pages = _dims(page_table, 2, "page_table")
-    _shape(k_pages, (L, n_pages, page_tokens, HEADS, HEAD_DIM), "k_pages")
-    _shape(v_pages, k_pages.shape, "v_pages")
-    _shape(q_off, (B + 1,), "q_off")
-    _shape(kv_len, (B,), "kv_len")
-    return n_pages, page_tokens, B, max_pages
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device_index != dev:
+        raise ValueError("stream on %s, tensors on cuda:%d" % (stream.device, dev))
+    else:
+        s = stream.cuda_stream
+    f = getattr(lib(), fn)
+    if torch.cuda.current_device() == dev:
+        status = f(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, s)
+    if status != MSA_OK:
+        _check(fn, status)
 
 
 def msa_paged_append(k_new, v_new, q, q_off, kv_len, page_table, k_pages, v_pages, q_out, eps, theta, pos_off=None,
@@ -341,29 +359,25 @@ def msa_paged_append(k_new, v_new, q, q_off, kv_len, page_table, k_pages, v_page
     q_off [B+1], kv_len [B] (new tokens included), page_table [B][max_pages], pos_off [B] int32;
     k_pages, v_pages [L][n_pages][page_tokens][8][128]; w_k, w_q [L][128] or None (no norm)."""
     L, n_q = _dims(k_new, 4, "k_new")[:2]
-    n_pages, page_tokens, B, max_pages = _paged(k_pages, v_pages, page_table, q_off, kv_len, L)
-    Hq = 0 if q is None else _dims(q, 4, "q")[2]
-    _shape(k_new, (L, n_q, HEADS, HEAD_DIM), "k_new")
-    _shape(v_new, k_new.shape, "v_new")
+    pages = _dims(k_pages, 5, "k_pages")
+    n_pages, page_tokens = pages[1], pages[2]
+    B, max_pages = _dims(page_table, 2, "page_table")
+    _required(v_new=v_new, q_off=q_off, kv_len=kv_len, v_pages=v_pages)
     if q is None:
-        q_out = w_q = None
+        Hq, q_out, w_q = 0, None, None
     else:
-        _shape(q, (L, n_q, Hq, HEAD_DIM), "q")
-        if q_out is None:
-            raise ValueError("q_out is required")
-        _shape(q_out, q.shape, "q_out")
-    _shape(pos_off, (B,), "pos_off")
-    _shape(w_k, (L, HEAD_DIM), "w_k")
-    _shape(w_q, (L, HEAD_DIM), "w_q")
-    args = (L, B, n_q, Hq, _ptr(k_new, _BF16, "k_new"), _ptr(v_new, _BF16, "v_new"),
-            _ptr(q, _BF16, "q", allow_none=True), _ptr(q_off, _I32T, "q_off"), _ptr(kv_len, _I32T, "kv_len"),
-            _ptr(pos_off, _I32T, "pos_off", allow_none=True), _ptr(page_table, _I32T, "page_table"), max_pages,
-            page_tokens, n_pages, _ptr(w_k, _BF16, "w_k", allow_none=True), _ptr(w_q, _BF16, "w_q", allow_none=True),
-            float(eps), float(theta), _ptr(k_pages, _BF16, "k_pages"), _ptr(v_pages, _BF16, "v_pages"),
-            _ptr(q_out, _BF16, "q_out", allow_none=True))
-    dev, s = _one_device(stream, k_new, v_new, q, q_off, kv_len, pos_off, page_table, w_k, w_q, k_pages, v_pages, q_out)
-    with torch.cuda.device(dev):
-        _check("msa_paged_append", lib().msa_paged_append(*args, s))
+        Hq = _dims(q, 4, "q")[2]
+        _required(q_out=q_out)
+    dev = k_new.get_device()
+    new, pages, heads = (L, n_q, HEADS, HEAD_DIM), (L, n_pages, page_tokens, HEADS, HEAD_DIM), (L, n_q, Hq, HEAD_DIM)
+    _call("msa_paged_append", dev, stream, (
+        L, B, n_q, Hq, _on(dev, k_new, _BF16, new, "k_new"), _on(dev, v_new, _BF16, new, "v_new"),
+        _on(dev, q, _BF16, heads, "q"), _on(dev, q_off, _I32T, (B + 1,), "q_off"),
+        _on(dev, kv_len, _I32T, (B,), "kv_len"), _on(dev, pos_off, _I32T, (B,), "pos_off"),
+        _on(dev, page_table, _I32T, None, "page_table"), max_pages, page_tokens, n_pages,
+        _on(dev, w_k, _BF16, (L, HEAD_DIM), "w_k"), _on(dev, w_q, _BF16, (L, HEAD_DIM), "w_q"), float(eps),
+        float(theta), _on(dev, k_pages, _BF16, pages, "k_pages"), _on(dev, v_pages, _BF16, pages, "v_pages"),
+        _on(dev, q_out, _BF16, heads, "q_out")))
 
 
 def msa_paged_attend_workspace_size(n_layers, B, n_groups, n_q, Hq) -> int:
@@ -375,31 +389,28 @@ def msa_paged_attend(q, q_off, kv_len, page_table, k_pages, v_pages, scale, out,
     """q [L][n_q][Hq][128]; the cache as for msa_paged_append; grp_off [n_groups+1] (None: every
     sequence its own group), ctx_k, ctx_v [L][n_groups][max_ctx][8][128] and ctx_len [L][n_groups]
     (None: no memory context), pre_len [n_groups] or None; out [L][n_q][Hq][128], fp32 or bf16."""
-    L, n_q, Hq = _dims(q, 4, "q")[:3]
-    n_pages, page_tokens, B, max_pages = _paged(k_pages, v_pages, page_table, q_off, kv_len, L)
-    n_groups = B if grp_off is None else _dims(grp_off, 1, "grp_off")[0] - 1
-    max_ctx = 0 if ctx_k is None else _dims(ctx_k, 5, "ctx_k")[2]
-    _shape(q, (L, n_q, Hq, HEAD_DIM), "q")
+    heads = _dims(q, 4, "q")
+    L, n_q, Hq = heads[0], heads[1], heads[2]
+    pages = _dims(k_pages, 5, "k_pages")
+    n_pages, page_tokens = pages[1], pages[2]
+    B, max_pages = _dims(page_table, 2, "page_table")
     _dims(out, 4, "out")
-    _shape(out, q.shape, "out")
+    _required(q_off=q_off, kv_len=kv_len, v_pages=v_pages, workspace=workspace)
+    n_groups = B if grp_off is None else _dims(grp_off, 1, "grp_off")[0] - 1
     if ctx_k is None:
-        ctx_v = ctx_len = None
+        max_ctx, ctx_v, ctx_len = 0, None, None
     else:
-        _shape(ctx_k, (L, n_groups, max_ctx, HEADS, HEAD_DIM), "ctx_k")
-        if ctx_v is None or ctx_len is None:
-            raise ValueError("ctx_v and ctx_len are required with ctx_k")
-        _shape(ctx_v, ctx_k.shape, "ctx_v")
-        _shape(ctx_len, (L, n_groups), "ctx_len")
-    _shape(pre_len, (n_groups,), "pre_len")
-    args = (L, B, n_groups, n_q, Hq, _ptr(q, _BF16, "q"), _ptr(q_off, _I32T, "q_off"),
-            _ptr(grp_off, _I32T, "grp_off", allow_none=True), _ptr(ctx_k, _BF16, "ctx_k", allow_none=True),
-            _ptr(ctx_v, _BF16, "ctx_v", allow_none=True), _ptr(ctx_len, _I32T, "ctx_len", allow_none=True), max_ctx,
-            _ptr(k_pages, _BF16, "k_pages"), _ptr(v_pages, _BF16, "v_pages"), n_pages, page_tokens,
-            _ptr(page_table, _I32T, "page_table"), max_pages, _ptr(kv_len, _I32T, "kv_len"),
-            _ptr(pre_len, _I32T, "pre_len", allow_none=True), float(scale), 0 if out.dtype == torch.float32 else 1,
-            _ptr(out, _F32_BF16, "out"), _ptr(workspace, _ANY, "workspace"),
-            workspace.numel() * workspace.element_size())
-    dev, s = _one_device(stream, q, q_off, kv_len, page_table, k_pages, v_pages, out, workspace, grp_off, ctx_k, ctx_v,
-                         ctx_len, pre_len)
-    with torch.cuda.device(dev):
-        _check("msa_paged_attend", lib().msa_paged_attend(*args, s))
+        max_ctx = _dims(ctx_k, 5, "ctx_k")[2]
+        _required(ctx_v=ctx_v, ctx_len=ctx_len)
+    dev = q.get_device()
+    heads, pages = (L, n_q, Hq, HEAD_DIM), (L, n_pages, page_tokens, HEADS, HEAD_DIM)
+    ctx = (L, n_groups, max_ctx, HEADS, HEAD_DIM)
+    _call("msa_paged_attend", dev, stream, (
+        L, B, n_groups, n_q, Hq, _on(dev, q, _BF16, heads, "q"), _on(dev, q_off, _I32T, (B + 1,), "q_off"),
+        _on(dev, grp_off, _I32T, None, "grp_off"), _on(dev, ctx_k, _BF16, ctx, "ctx_k"),
+        _on(dev, ctx_v, _BF16, ctx, "ctx_v"), _on(dev, ctx_len, _I32T, (L, n_groups), "ctx_len"), max_ctx,
+        _on(dev, k_pages, _BF16, pages, "k_pages"), _on(dev, v_pages, _BF16, pages, "v_pages"), n_pages, page_tokens,
+        _on(dev, page_table, _I32T, None, "page_table"), max_pages, _on(dev, kv_len, _I32T, (B,), "kv_len"),
+        _on(dev, pre_len, _I32T, (n_groups,), "pre_len"), float(scale), 0 if out.dtype == torch.float32 else 1,
+        _on(dev, out, _F32_BF16, heads, "out"), _on(dev, workspace, _ANY, None, "workspace"),
+        workspace.numel() * workspace.element_size()))
