@@ -922,6 +922,12 @@ static_assert(kStage == 2 * kTileRows * 16, "K rows and V rows");
 typedef __attribute__((address_space(1))) const void* gptr_t;
 typedef __attribute__((address_space(3))) void* lptr_t;
 
+// A stage chosen at run time.
+__device__ __forceinline__ uint32_t lds_at(u32x4* p) { return (uint32_t)(uintptr_t)(lptr_t)p; }
+__device__ __forceinline__ const u32x4* lds_ptr(uint32_t at) {
+  return (const u32x4*)(__attribute__((address_space(3))) const u32x4*)(uintptr_t)at;
+}
+
 // This lane's pieces of K and V fragments in a stage.
 struct StageReads {
   int k0, v0;
@@ -939,9 +945,9 @@ struct StageReads {
   }
 };
 
-// The rows of N stages into the state; a column sees the first left[u] of each (whole: all of all).  Two at once
-// make one decision about the maximum for 64 rows, and the second tile's scores are formed while the
-// first one's settle.
+// The rows of N stages into the state; a column sees the first left_a and left_b of them (whole: all of all).  Two
+// at once make one decision about the maximum for 64 rows, and the second tile's scores are formed while
+// the first one's settle.
 template <int PARTS, bool CAREFUL, int N>
 __device__ __forceinline__ void attend_tiles(const u32x4* stage_a, const u32x4* stage_b, const StageReads& at, const u32x4* qf,
                                              bool whole, int32_t left_a, int32_t left_b, float scale2, int h, State& st) {
@@ -1004,7 +1010,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
   const int32_t blocks = uni(it.blocks), unit = uni(it.unit), share = kWaves / blocks;
   const int32_t tile0 = uni(it.tile0), head = uni(it.head);
   int32_t tile1 = uni(it.tile1);
-  const int cb = wave & (blocks - 1), turn = wave / blocks;
+  const int cb = wave & (blocks - 1), turn = uni(wave / blocks);
   const Column y = column_of(a, x, layer, head, it.col0 + cb * kCols + c);
   int32_t limit = 0;                                 // first local row (from p0) the column does not see
   if (y.live && x.p1 > x.p0) {
@@ -1116,29 +1122,47 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
     }
     attend_tiles<PARTS, false, 1>(stage, stage, at, qf, whole(t), left_of(t), 0, a.scale2, h, st);
   };
-  // Fewer blocks, bound by the rows' bytes: two tiles a step, for one of the block's waves.  An odd last tile comes
-  // with a copy of itself that nothing sees.
-  auto pair = [&](int32_t t, const u32x4* a0, const u32x4* a1, u32x4* b0, u32x4* b1) __attribute__((always_inline)) {
-    __builtin_amdgcn_s_waitcnt(kWaitAll);
-    asm volatile("s_barrier" ::: "memory");
-    if (t + 2 < tile1) {
-      issue(t + 2, page_a, b0);
-      issue(min(t + 3, last), page_b, b1);
-      find(min(t + 4, last), page_a);
-      find(min(t + 5, last), page_b);
+  // Fewer blocks, bound by the rows' bytes: four tiles a step, one or two for each wave, and the next four only
+  // once all are done: the other workgroup of the CU computes or loads meanwhile.  (Two tiles in use and two on
+  // their way, one wave computing at a time: 78 us for 46 tiles of 64 columns, so 56.)  A tile behind the last
+  // is a copy of it that nothing sees.
+  int32_t pages[kWaves];
+  auto issue_all = [&](int32_t t) __attribute__((always_inline)) {
+    issue(t, pages[0], stage0);
+    issue(min(t + 1, last), pages[1], stage1);
+    issue(min(t + 2, last), pages[2], stage2);
+    issue(min(t + 3, last), pages[3], stage3);
+  };
+  auto find_all = [&](int32_t t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) find(min(t + i, last), pages[i]);
+  };
+  auto steps = [&](auto per) __attribute__((always_inline)) {
+    constexpr int N = decltype(per)::value;
+    const uint32_t from = turn * N, a0 = lds_at(stage0), a1 = lds_at(stage1), a2 = lds_at(stage2), a3 = lds_at(stage3);
+    const u32x4* sa = lds_ptr(from == 0 ? a0 : (from == 1 ? a1 : (from == 2 ? a2 : a3)));
+    const u32x4* sb = N == 2 ? lds_ptr(from == 0 ? a1 : a3) : sa;
+    for (int32_t t = tile0;; t += kWaves) {
+      __builtin_amdgcn_s_waitcnt(kWaitAll);
+      asm volatile("s_barrier" ::: "memory");
+      const int32_t u = t + N * turn;
+      if (u < tile1)
+        attend_tiles<PARTS, false, N>(sa, sb, at, qf, u + N - 1 < tile1 && whole(u) && whole(u + N - 1), left_of(u),
+                                      u < last ? left_of(u + 1) : 0, a.scale2, h, st);
+      if (t + kWaves >= tile1) break;
+      asm volatile("s_barrier" ::: "memory");
+      issue_all(t + kWaves);
+      find_all(t + 2 * kWaves);
     }
-    if (((t >> 1) & (share - 1)) == turn)
-      attend_tiles<PARTS, false, 2>(a0, a1, at, qf, t < last && whole(t) && whole(t + 1), left_of(t),
-                                    t < last ? left_of(t + 1) : 0, a.scale2, h, st);
   };
   if (tile0 < tile1) {
-    find(tile0, page_a);
-    find(min(tile0 + 1, last), page_b);
-    issue(tile0, page_a, stage0);
-    issue(min(tile0 + 1, last), page_b, stage1);
-    find(min(tile0 + 2, last), page_a);
-    find(min(tile0 + 3, last), page_b);
     if (blocks == kWaves) {
+      find(tile0, page_a);
+      find(min(tile0 + 1, last), page_b);
+      issue(tile0, page_a, stage0);
+      issue(min(tile0 + 1, last), page_b, stage1);
+      find(min(tile0 + 2, last), page_a);
+      find(min(tile0 + 3, last), page_b);
       if (tile0 + 2 < tile1) issue(tile0 + 2, page_a, stage2);
       page_a = page_b;
       for (int32_t t = tile0; t < tile1; t += 4) {
@@ -1148,10 +1172,11 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
         if (t + 3 < tile1) step(t + 3, stage3, stage2);
       }
     } else {
-      for (int32_t t = tile0; t < tile1; t += 4) {
-        pair(t, stage0, stage1, stage2, stage3);
-        if (t + 2 < tile1) pair(t + 2, stage2, stage3, stage0, stage1);
-      }
+      find_all(tile0);
+      issue_all(tile0);
+      find_all(tile0 + kWaves);
+      if (blocks == 2) steps(std::integral_constant<int, 2>());
+      else steps(std::integral_constant<int, 1>());
     }
   }
   if (__syncthreads_or(holds_nan(st))) {
@@ -1162,7 +1187,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
       issue(t, page_a, stage0);
       __builtin_amdgcn_s_waitcnt(kWaitAll);
       __syncthreads();
-      if (((t >> 1) & (share - 1)) == turn)
+      if ((t & (share - 1)) == turn)
         attend_tiles<PARTS, true, 1>(stage0, stage0, at, qf, false, left_of(t), 0, a.scale2, h, st);
       __syncthreads();
     }
@@ -1203,7 +1228,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
 
 template <bool BF16_OUT>
 __global__ void __launch_bounds__(kThreads, 2)
-attend_kernel(const AttendArgs a, const uint32_t L) {
+attend_kernel(const AttendArgs a) {
   __shared__ u32x4 stage0[kStage], stage1[kStage], stage2[kStage], stage3[kStage];
   __shared__ union {
     ItemShared item;
@@ -1214,11 +1239,11 @@ attend_kernel(const AttendArgs a, const uint32_t L) {
   } sh;
   const int tid = threadIdx.x;
   // layers fastest: the workgroups that turn out to have nothing to do come last
-  const int64_t layer = blockIdx.x % L;
+  const int64_t layer = blockIdx.x;
   const Lengths n = lengths_in(stage0, stage1, stage2, stage3);
   load_lengths(a, n, layer, tid);
   const Plan p = make_plan(a, n, tid);
-  const uint32_t id = blockIdx.x / L;
+  const uint32_t id = blockIdx.z * gridDim.y + blockIdx.y;
   // items that fit the chip at once are the longer ones; items of many rounds end more evenly than shares
   const bool items_first = p.all_items <= (uint32_t)a.both_wgs;
   const uint32_t first_share = items_first ? p.all_items : 0, first_item = items_first ? 0 : p.shares;
@@ -1349,7 +1374,8 @@ size_t attend_workspace_bytes(int32_t L, int32_t B, int32_t n_groups, int32_t n_
 
 template <bool BF16_OUT>
 static void launch_attend_as(const AttendArgs& a, const Sizes& z, int32_t L, hipStream_t s) {
-  hipLaunchKernelGGL(attend_kernel<BF16_OUT>, dim3((unsigned)(L * (int64_t)z.grid)), dim3(kThreads), 0, s, a, (uint32_t)L);
+  const unsigned most = 32768, y = (unsigned)z.grid < most ? (unsigned)z.grid : most;    // a launch's y may have 65,535
+  hipLaunchKernelGGL(attend_kernel<BF16_OUT>, dim3((unsigned)L, y, (z.grid + y - 1) / y), dim3(kThreads), 0, s, a);
   // a workgroup for 8 heads of one token, of several (at most 64) where there are many
   const int64_t rows = (int64_t)a.n_q * a.G * L;
   const int32_t per = (int32_t)(rows < 8192 ? 1 : (rows > 64 * 8192 ? 64 : rows / 8192));

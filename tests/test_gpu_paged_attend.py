@@ -168,6 +168,40 @@ def test_many_sequences():
     check_attention(b, attend(b), tokens=some(b, 150))
 
 
+@pytest.mark.parametrize("groups,pre", [([7], [64]), ([3, 4], [32, 0]), ([1, 5, 1], [0, 64, 9])])
+def test_long_sequences_among_short_ones_of_a_group(groups, pre):
+    """One at the border (512 columns) and some past it, which read their group's rows themselves."""
+    print("case: long sequences in groups", groups, flush=True)
+    new = [1, 200, 1, 1, 130, 129, 128]
+    ctx = [[100, 33, 70][:len(groups)]]
+    b = Batch(new, [n + 70 + s for s, n in enumerate(new)], groups=groups, ctx=ctx, pre=pre, page=32, hq=32, pad=2,
+              seed=95, q_std=2.0)
+    check_attention(b, attend(b), tokens=some(b, 40))
+    check_attention(b, attend(b, dtype=BF16), tokens=some(b, 40))
+
+
+@pytest.mark.parametrize("groups", [None, 7])
+def test_many_short_sequences_in_many_layers(groups):
+    """More pieces in a workgroup's share of the rows than it lists at a time."""
+    print("case: short sequences, many layers", groups, flush=True)
+    rng = np.random.default_rng(17)
+    new = rng.choice([0, 1, 1, 2], 700).tolist()
+    rows = [n + int(rng.integers(0, 70)) for n in new]
+    if groups:
+        b = Batch(new, rows, groups=[groups] * 100, ctx=rng.integers(0, 40, (24, 100)).tolist(), page=16, hq=8, layers=24,
+                  seed=96)
+    else:
+        b = Batch(new, rows, page=16, hq=8, layers=24, seed=97)
+    check_attention(b, attend(b), tokens=some(b, 150))
+
+
+def test_many_prompts():
+    """2,048 prompts of 64 tokens and 64 query heads: more workgroups than one dimension of a launch holds."""
+    print("case: 2048 prompts", flush=True)
+    b = Batch([64] * 2048, [64 + s % 3 for s in range(2048)], page=64, hq=64, seed=98)
+    check_attention(b, attend(b, dtype=BF16), tokens=some(b, 60))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 3.3e38])
 def test_rows_out_of_sight_do_not_reach_the_output(bad, dtype):
