@@ -269,19 +269,19 @@ __device__ __forceinline__ void scan2(const Lengths& n, int slot, uint32_t& x, u
 // it.  State16: column l & 15, dims 16 d + 4 (l >> 4) + r.
 struct State {
   static constexpr int kBlocks = 4, kRegs = 16;
-  float m, l;
+  float m, l, neg;     // neg: -m, 0 for no row so far
   f32x16 o[4];
 };
 struct State16 {
   static constexpr int kBlocks = 8, kRegs = 4;
-  float m, l;
+  float m, l, neg;
   f32x4 o[8];
 };
 
 template <typename St>
 __device__ __forceinline__ void clear(St& st) {
   st.m = -__builtin_huge_valf();
-  st.l = 0.f;
+  st.l = st.neg = 0.f;
 #pragma unroll
   for (int d = 0; d < St::kBlocks; ++d)
 #pragma unroll
@@ -339,9 +339,11 @@ __device__ __forceinline__ u32x4 without_specials(u32x4 raw, u32x4 bad, u32x4 p,
 }
 
 // A masked row's weight is 0, but 0 * inf is NaN (and with probabilities in three parts, an infinity meets a
-// residual of either sign).  So when what was summed up holds NaN, it is gone through once more with
-// CAREFUL set, where V entries that are no finite numbers are taken out of the products: that gives
-// what the columns see and nothing else.
+// residual of either sign).  A weight above 1 (below) may overflow with values near the largest, and a
+// maximum beyond 2^29 is rounded by more than the weights' range bears.  So when what was summed up is not
+// finite, or the maximum that large, it is gone through once more with CAREFUL set: V entries that are no finite
+// numbers are taken out of the products, the maximum is always the largest score, and the scores are
+// rounded as it is.
 
 __device__ __forceinline__ f32x16 zeros16() {
   return f32x16{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -361,21 +363,29 @@ __device__ __forceinline__ float max16(const f32x16& s) {
   return m;
 }
 
-// The running maximum (log2 units) against a tile's largest score: it is raised only when the tile passes
-// it by more than 2^8, so most tiles skip the rescale.
-template <typename St>
+// The running maximum (log2 units) against a tile's largest score: it is raised only when the tile passes it by
+// more than 2^8, so most tiles skip the rescale (a prompt of 8,000 tokens 1.18 ms, 1.25 raising it always).
+template <bool CAREFUL, typename St>
 __device__ __forceinline__ void raise_to(float mt, float scale2, St& st) {
   const float ninf = -__builtin_huge_valf();
   mt *= scale2;
-  const bool raise = mt > st.m + 8.f;
+  const bool raise = mt > st.m + (CAREFUL ? 0.f : 8.f);
   if (__builtin_expect(__ballot(raise) != 0, 0)) {
     const float mn = raise ? mt : st.m;
     const float alpha = st.m == ninf ? (raise ? 0.f : 1.f) : __builtin_amdgcn_exp2f(st.m - mn);
     st.m = mn;
+    st.neg = mn == ninf ? 0.f : -mn;
     st.l *= alpha;
 #pragma unroll
     for (int d = 0; d < St::kBlocks; ++d) st.o[d] *= alpha;
   }
+}
+
+// A score's distance to the maximum.
+template <bool CAREFUL>
+__device__ __forceinline__ float below(float s, float scale2, float neg_m) {
+#pragma clang fp contract(off)
+  return CAREFUL ? s * scale2 + neg_m : __builtin_fmaf(s, scale2, neg_m);
 }
 
 // Probabilities of 8 scores as a B operand of the second product, and into the sum.
@@ -384,12 +394,12 @@ __device__ __forceinline__ void raise_to(float mt, float scale2, St& st) {
 // against 985 us where the matrix cores bind (8 prompts of up to 1,088 tokens, 4 layers), next to nothing elsewhere.
 // PARTS 1 (bf16 output): one bf16 value, whose rounding (2^-8 of each weight) is the size of the
 // output's own; the sum is then taken of the rounded values, so the weights still add up to one.
-template <int PARTS>
+template <int PARTS, bool CAREFUL>
 __device__ __forceinline__ void weights(const float* s, float scale2, float neg_m, u32x4* pw, float& l) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * e], scale2, neg_m));
-    const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * e + 1], scale2, neg_m));
+    const float p0 = __builtin_amdgcn_exp2f(below<CAREFUL>(s[2 * e], scale2, neg_m));
+    const float p1 = __builtin_amdgcn_exp2f(below<CAREFUL>(s[2 * e + 1], scale2, neg_m));
     const uint32_t w = pack2_bf16(p0, p1);
     pw[0][e] = w;
     if (PARTS > 1) {
@@ -421,12 +431,13 @@ __device__ __forceinline__ void add_values(u32x4 vf, const u32x4* pw, Acc& o) {
 }
 
 template <typename St>
-__device__ __forceinline__ bool holds_nan(const St& st) {
-  bool odd = false;
+__device__ __forceinline__ bool needs_care(const St& st) {
+  const float inf = __builtin_huge_valf();
+  bool odd = st.m != -inf && __builtin_fabsf(st.m) >= 0x1p29f;
 #pragma unroll
   for (int d = 0; d < St::kBlocks; ++d)
 #pragma unroll
-    for (int r = 0; r < St::kRegs; ++r) odd |= st.o[d][r] != st.o[d][r];
+    for (int r = 0; r < St::kRegs; ++r) odd |= !(__builtin_fabsf(st.o[d][r]) < inf);
   return __ballot(odd) != 0;
 }
 
@@ -744,9 +755,9 @@ __device__ __forceinline__ void attend_rows(uint16_t* tile, const u32x4* pv, con
     v[e] = 16 * (e >> 2) + 4 * g + (e & 3) < left ? s[e >> 2][e & 3] : -__builtin_huge_valf();
     mt = fmaxf(mt, v[e]);
   }
-  raise_to(rows4_max(mt), scale2, st);
+  raise_to<CAREFUL>(rows4_max(mt), scale2, st);
   u32x4 pw[PARTS];
-  weights<PARTS>(v, scale2, st.m == -__builtin_huge_valf() ? 0.f : -st.m, pw, st.l);
+  weights<PARTS, CAREFUL>(v, scale2, st.neg, pw, st.l);
   // a 16-lane group reads 16 dims of 4 rows transposed
   const uint16_t* vsrc = tile + (4 * g + (j >> 2)) * kVStride + 4 * (j & 3);
 #pragma unroll
@@ -882,7 +893,7 @@ __device__ __forceinline__ void attend_streams(const AttendArgs& a, const Length
           }
         });
       }
-      if (holds_nan(st)) {
+      if (needs_care(st)) {
         clear(st);
         Cursor u = l;
         enter(u, s);
@@ -958,12 +969,12 @@ struct StageReads {
   }
 };
 
-// The rows of N stages into the state; a column sees the first left_a and left_b of them (whole: all of all).  Two
+// The rows of N stages into the state; a column sees the first left(u) of them (whole: all of all).  Two
 // at once make one decision about the maximum for 64 rows, and the second tile's scores are formed while
 // the first one's settle.  kf: the K fragments of a single tile where they have been read already.
-template <int PARTS, bool CAREFUL, int N>
+template <int PARTS, bool CAREFUL, int N, typename Left>
 __device__ __forceinline__ void attend_tiles(const u32x4* kf, const u32x4* stage_a, const u32x4* stage_b, const StageReads& at, const u32x4* qf,
-                                             bool whole, int32_t left_a, int32_t left_b, float scale2, int h, State& st) {
+                                             bool whole, Left&& left, float scale2, int h, State& st) {
   f32x16 s[N];
 #pragma unroll
   for (int u = 0; u < N; ++u) {
@@ -980,13 +991,12 @@ __device__ __forceinline__ void attend_tiles(const u32x4* kf, const u32x4* stage
   }
   if (!whole) {
     asm volatile("" ::: );      // a branch: most tiles are whole, and selects for all would cost what the exps do
-    mask_rows(s[0], left_a, h);
-    if (N == 2) mask_rows(s[N - 1], left_b, h);
+    mask_rows(s[0], left(0), h);
+    if (N == 2) mask_rows(s[N - 1], left(1), h);
   }
   float top = max16(s[0]);
   if (N == 2) top = fmaxf(top, max16(s[N - 1]));
-  raise_to(halves_max(top), scale2, st);
-  const float neg_m = st.m == -__builtin_huge_valf() ? 0.f : -st.m;
+  raise_to<CAREFUL>(halves_max(top), scale2, st);
 #pragma unroll
   for (int u = 0; u < N; ++u)
 #pragma unroll
@@ -996,7 +1006,7 @@ __device__ __forceinline__ void attend_tiles(const u32x4* kf, const u32x4* stage
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = s[u][8 * m + e];
       u32x4 pw[PARTS];
-      weights<PARTS>(v, scale2, neg_m, pw, st.l);
+      weights<PARTS, CAREFUL>(v, scale2, st.neg, pw, st.l);
 #pragma unroll
       for (int d = 0; d < 4; ++d)
         add_values<PARTS, CAREFUL>(CAREFUL || u ? at.v(u ? stage_b : stage_a, m, d) : vf[m][d], pw, st.o[d]);
@@ -1062,18 +1072,22 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
   constexpr int kPer = kTileRows / 4 / kWaves;
   const int64_t ctx_at = (layer * a.n_groups + uni(x.grp)) * (int64_t)a.max_ctx * kRow + head * kDim;
   const int64_t page_at = ((layer * a.n_pages) << a.page_shift) * kRow + head * kDim;
-  const uint16_t *ctx_k = kept(a.ctx_k + ctx_at), *ctx_v = kept(a.ctx_v + ctx_at);
-  const uint16_t *page_k = kept(a.k_pages + page_at), *page_v = kept(a.v_pages + page_at);
+  const char *ctx_k = kept((const char*)(a.ctx_k + ctx_at)), *ctx_v = kept((const char*)(a.ctx_v + ctx_at));
+  const char *page_k = kept((const char*)(a.k_pages + page_at)), *page_v = kept((const char*)(a.v_pages + page_at));
   const auto* table = (const __attribute__((address_space(4))) int32_t*)kept(a.page_table + (int64_t)seq * a.max_pages);
   const int32_t shift = kept(a.page_shift), last_page = kept(a.n_pages - 1);
   const int w8 = uni(4 * kPer * wave);
-  const bool eights = shift >= 3 && (p0 & 7) == 0;
+  // the memory rows' partial tile, if they have one; the end of the tiles whose rows are found by eights, of
+  // those that all the wave's columns see
+  const int32_t odd = jc & (kTileRows - 1) ? nctx - 1 : -1;
+  const int32_t eights_end = nctx + (shift >= 3 && (p0 & 7) == 0 ? wg_most / kTileRows : 0);
+  const int32_t whole_end = nctx + min(wg_most, least) / kTileRows;
   uint32_t k_lane[kPer], v_lane[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int r = 4 * i + (lane >> 4);
-    k_lane[i] = r * kRow + 8 * ((lane & 15) ^ ((w8 + r) & 15));
-    v_lane[i] = r * kRow + 8 * ((lane & 15) ^ (4 * (lane >> 4)));
+    k_lane[i] = 2 * (r * kRow + 8 * ((lane & 15) ^ ((w8 + r) & 15)));
+    v_lane[i] = 2 * (r * kRow + 8 * ((lane & 15) ^ (4 * (lane >> 4))));
   }
   // the page of the wave's rows of a page tile, as it stands in the table: a scalar load (a vector load's result
   // would only come after all the tile loads issued before it), not waited for before the tile's turn
@@ -1087,17 +1101,19 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
   };
   auto issue = [&](int32_t t, int32_t page, u32x4* stage) __attribute__((always_inline)) {
     const bool ctx = t < nctx;
-    const uint16_t *kb = ctx ? ctx_k : page_k, *vb = ctx ? ctx_v : page_v;
-    u32x4* to = stage + kPer * wave * 64;
-    if (ctx ? (t + 1) * kTileRows <= jc : eights && (t - nctx + 1) * kTileRows <= wg_most) {
+    const char *kb = ctx ? ctx_k : page_k, *vb = ctx ? ctx_v : page_v;
+    u32x4* to = stage + kPer * 64 * (w8 / (4 * kPer));
+    if (t != odd && t < eights_end) {
       int32_t row = t * kTileRows + w8;
       if (!ctx) row = (clampi(page, 0, last_page) << shift) + (local_row(t) & ((1 << shift) - 1));
-      const int64_t at = (int64_t)row * kRow;
+      kb += (int64_t)row * (2 * kRow);
+      vb += (int64_t)row * (2 * kRow);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        __builtin_amdgcn_global_load_lds((gptr_t)(kb + at + k_lane[i]), (lptr_t)(to + 64 * i), 16, 0, 0);
-        __builtin_amdgcn_global_load_lds((gptr_t)(vb + at + v_lane[i]), (lptr_t)(to + 64 * i + kTileRows * 16), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((gptr_t)(kb + k_lane[i]), (lptr_t)(to + 64 * i), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((gptr_t)(vb + v_lane[i]), (lptr_t)(to + 64 * i + kTileRows * 16), 16, 0, 0);
       }
+      asm volatile("" ::: );      // keeps the two branches' loads apart: these have scalar bases
     } else {
       int by = lane >> 4;
       asm volatile("" : "+v"(by));          // what follows is not kept in registers from tile to tile
@@ -1106,7 +1122,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
         const int r = 4 * i + by;
         const int32_t row = ctx ? min(t * kTileRows + w8 + r, jc - 1)
                                 : page_row(a, seq, p0 + min((t - nctx) * kTileRows + w8 + r, wg_most - 1));
-        const int64_t at = (int64_t)(row - r) * kRow;
+        const int64_t at = (int64_t)(row - r) * (2 * kRow);
         __builtin_amdgcn_global_load_lds((gptr_t)(kb + at + k_lane[i]), (lptr_t)(to + 64 * i), 16, 0, 0);
         __builtin_amdgcn_global_load_lds((gptr_t)(vb + at + v_lane[i]), (lptr_t)(to + 64 * i + kTileRows * 16), 16, 0, 0);
       }
@@ -1120,7 +1136,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
     return t < nctx ? jc - t * kTileRows : limit - (t - nctx) * kTileRows;
   };
   auto whole = [&](int32_t t) __attribute__((always_inline)) {
-    return (t < nctx ? jc - t * kTileRows : min(wg_most, least) - (t - nctx) * kTileRows) >= kTileRows;
+    return t != odd && t < whole_end;
   };
   const int32_t last = tile1 - 1;
   // Four column blocks, bound by the matrix cores and the vector work: one tile a step.  This wave's loads of it
@@ -1139,7 +1155,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
       issue(t + 3, page_a, before);
       find(min(t + 4, last), page_a);
     }
-    attend_tiles<PARTS, false, 1>(kf, stage, stage, at, qf, whole(t), left_of(t), 0, a.scale2, h, st);
+    attend_tiles<PARTS, false, 1>(kf, stage, stage, at, qf, whole(t), [&](int) __attribute__((always_inline)) { return left_of(t); }, a.scale2, h, st);
   };
   // Fewer blocks, bound by the rows' bytes: four tiles a step, one or two for each wave, and the next four only
   // once all are done: the other workgroup of the CU computes or loads meanwhile.  (Two tiles in use and two on
@@ -1166,8 +1182,9 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
       asm volatile("s_barrier" ::: "memory");
       const int32_t u = t + N * turn;
       if (u < tile1)
-        attend_tiles<PARTS, false, N>(nullptr, sa, sb, at, qf, u + N - 1 < tile1 && whole(u) && whole(u + N - 1), left_of(u),
-                                      u < last ? left_of(u + 1) : 0, a.scale2, h, st);
+        attend_tiles<PARTS, false, N>(nullptr, sa, sb, at, qf, u + N - 1 < tile1 && whole(u) && whole(u + N - 1), [&](int v) __attribute__((always_inline)) {
+          return u + v < tile1 ? left_of(u + v) : 0;
+        }, a.scale2, h, st);
       if (t + kWaves >= tile1) break;
       asm volatile("s_barrier" ::: "memory");
       issue_all(t + kWaves);
@@ -1198,7 +1215,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
       else steps(std::integral_constant<int, 1>());
     }
   }
-  if (__syncthreads_or(holds_nan(st))) {
+  if (__syncthreads_or(needs_care(st))) {
     clear(st);
 #pragma unroll 1
     for (int32_t t = tile0; t < tile1; ++t) {
@@ -1207,7 +1224,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
       __builtin_amdgcn_s_waitcnt(kWaitAll);
       __syncthreads();
       if ((t & (share - 1)) == turn)
-        attend_tiles<PARTS, true, 1>(nullptr, stage0, stage0, at, qf, false, left_of(t), 0, a.scale2, h, st);
+        attend_tiles<PARTS, true, 1>(nullptr, stage0, stage0, at, qf, false, [&](int) __attribute__((always_inline)) { return left_of(t); }, a.scale2, h, st);
       __syncthreads();
     }
   }

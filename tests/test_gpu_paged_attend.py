@@ -261,6 +261,50 @@ def test_large_scores():
         check_attention(b, attend(b, scale=scale), scale=scale)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_in_the_billions(sign, dtype):
+    """Each more than 2^27 from the next (in log2 units): the output is the V row of the largest score."""
+    print("case: scores in the billions", sign, dtype, flush=True)
+    new, rows = [1, 10, 40], [200, 150, 170]
+    b = Batch(new, rows, page=16, hq=32, seed=123)
+    rng = np.random.default_rng(123)
+    b.q.zero_()
+    b.q[..., 0] = 2.0 ** 20
+    order = []
+    for s in range(3):
+        steps = rng.permutation(256)[:rows[s]] + 1
+        order.append(steps)
+        for r in range(rows[s]):
+            pg, rw = b.spot(s, r)
+            b.k_pages[0, pg, rw] = 0
+            b.k_pages[0, pg, rw, :, 0] = float(sign * steps[r]) * 2.0 ** 12
+    out = attend(b, dtype=dtype).cpu()
+    for s in range(3):
+        for i in range(new[s]):
+            r = int(np.argmax(sign * order[s][:rows[s] - new[s] + i + 1]))
+            pg, rw = b.spot(s, r)
+            v = b.v_pages[0, pg, rw].repeat_interleave(4, 0)
+            assert torch.equal(out[0, b.q_off[s] + i], v.to(dtype)), (s, i)
+
+
+def test_values_near_the_largest():
+    """A row that the running maximum, not yet raised, gives a weight of 2^7, with values near the largest."""
+    print("case: values near the largest", flush=True)
+    new, rows = [1, 10, 40], [100, 100, 100]
+    b = Batch(new, rows, page=16, hq=32, seed=124)
+    b.q.zero_()
+    b.q[..., 0] = 1.0
+    for s in range(3):
+        for r in range(rows[s]):
+            pg, rw = b.spot(s, r)
+            b.k_pages[0, pg, rw, :, 0] = 55.0 if r == 40 else 0.0       # 7.01 / (scale log2 e)
+            if r == 40:
+                b.v_pages[0, pg, rw] = 2.9e38
+    for dtype in (F32, BF16):
+        check_attention(b, attend(b, dtype=dtype))
+
+
 def test_rising_scores_move_the_maximum():
     """Keys ordered so that the running maximum rises with almost every tile."""
     print("case: rising scores", flush=True)
