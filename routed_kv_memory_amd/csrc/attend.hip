@@ -19,7 +19,12 @@
 // - more columns are bound by the matrix cores and the softmax's vector work: 4 waves take one head and
 //   share each tile of 32 rows, 32 columns a wave (attend_item).
 // attend_join_kernel joins where a column's rows were cut into parts; what is whole in one part has been
-// written by the workgroup that computed it.
+// written by the workgroup that computed it.  (A workgroup that joins for the others would need a counter and
+// a device-wide release in each; the launch costs ~5 us.)
+// Measured: one token of 32 heads over 4,364 rows in 18 layers 61 us (4.9 TB/s); a prompt of 8,000 tokens
+// over 4,300 memory rows 1.03-1.12 ms (960-1,044 TFLOP/s, bf16 output), matrix cores 41% busy and vector units 43%, which
+// overlap little; each scalar or vector instruction between a tile's barrier and its last product
+// still shows in the time.
 // In both, S^T = K . Q^T is computed with K as the A operand and the columns as the B operand
 // (registers), so a lane holds scores of one column and the softmax needs only exchanges between the
 // lane groups of a wave; for O^T += V^T . P^T the MFMA's k axis is taken in the order in which the scores
@@ -37,10 +42,14 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kStreamCols = 16;           // columns of a wave that streams, and most of such a job
+// Columns of a wave that streams, and most of such a job.  Two such blocks in a wave take more registers than it
+// has (a step of 16 samples, 32 columns of 8 share their rows: 205 against 164 us); the other way round, 16
+// samples' own rows (4 columns each) as shared tiles take 254 against 166 us.
+constexpr int kStreamCols = 16;
 constexpr int kCols = 32;                 // columns of a wave that shares tiles
 // A sequence of more columns than this does not share its group's rows: parts of so many columns cost
-// more to write and join than the rows cost to read again.
+// more to write and join than the rows cost to read again (three sequences of 509 tokens, 32 heads, among 27 of
+// one token over 1,500 shared rows: 195 us, 256 us sharing; from 128 to 512 it is the same).
 constexpr int kAlone = 512;
 constexpr int kWide = kWaves * kCols;     // columns of a workgroup of the second kind
 constexpr int kSets = kHeads / kWaves;    // head sets of a streamed job: streams of rows it makes
@@ -54,7 +63,8 @@ constexpr int kMaxSeqs = 2048;            // MSA_MAX_SEQS
 constexpr int kSegments = 32;             // pieces of streams a workgroup lists at a time
 // Two workgroups fit a CU (registers, LDS): 512 fill the chip.  A layer gets its share of them, but at
 // least kBothWgs where there are jobs of both kinds: items come in eights (the heads), and a handful of
-// eights would not split the work evenly.
+// eights would not split the work evenly.  16 samples of one question, 18 layers: 199 us with 28, 175 with 40,
+// 173 with 56, 186 with 64, 182 with 72.
 constexpr int kWgs = 512;
 constexpr int kBothWgs = 56;
 
@@ -460,7 +470,8 @@ __device__ __forceinline__ Column column_of(const AttendArgs& a, const Job& x, i
 }
 
 // Four dims from `d` on of a column: into a part of the workspace (the index of its column there) or the output.
-__device__ __forceinline__ void write_part(const AttendArgs& a, int64_t part, int d, float v0, float v1, float v2, float v3) {
+__device__ __forceinline__ void write_part(const AttendArgs& a, int64_t part, int d, float v0, float v1, float v2,
+                                           float v3) {
   *reinterpret_cast<float4*>(a.acc + part * kDim + d) = make_float4(v0, v1, v2, v3);
 }
 template <bool BF16_OUT>
@@ -501,7 +512,8 @@ __device__ __forceinline__ void write_state(const AttendArgs& a, const State16& 
 #pragma unroll
   for (int d = 0; d < 8; ++d) {
     if (unit >= 0) write_part(a, part, 16 * d + 4 * g, st.o[d][0], st.o[d][1], st.o[d][2], st.o[d][3]);
-    else write_out<BF16_OUT>(a, y.row, 16 * d + 4 * g, st.o[d][0] * inv, st.o[d][1] * inv, st.o[d][2] * inv, st.o[d][3] * inv);
+    else write_out<BF16_OUT>(a, y.row, 16 * d + 4 * g, st.o[d][0] * inv, st.o[d][1] * inv, st.o[d][2] * inv,
+                             st.o[d][3] * inv);
   }
 }
 
@@ -529,8 +541,9 @@ __device__ __forceinline__ void describe(const AttendArgs& a, const Job& x, cons
 // streams; a piece is one part of its columns.
 //
 // The other jobs make items: a column block of 128, one head, a chunk of the rows.  A job's rows are cut
-// into its share of the workgroups, rounded down, so that they all run at once, but into chunks of
-// eight tiles at least.  Of a job's items those of the last column blocks, whose tokens see the most rows,
+// into its share of the workgroups, rounded down, so that they all run at once (rounded to the nearest, 61
+// sequences behind 30,000 shared rows take 140 us, so 118), but into chunks of eight tiles at least
+// (four or sixteen measure the same).  Of a job's items those of the last column blocks, whose tokens see the most rows,
 // come first (workgroups start in order); heads fastest (workgroups go to the 8 XCDs in turn: a
 // head's rows stay in one L2).
 
@@ -590,7 +603,8 @@ __device__ __forceinline__ Plan make_plan(const AttendArgs& a, const Lengths& n,
   p.shares = a.wgs;
   if (work > 0.f) {                               // uniform
     // a streamed tile is 4 heads' rows, an item's is one head's, of more columns: 4.2 against 1.2 us where
-    // both wait for HBM, 2.7 against 1.3 next to items bound by the matrix cores
+    // both wait for HBM, 2.3 against 1.2 next to items bound by the matrix cores (2, 3 and 4 in place of
+    // one for the other measure the same within 3%)
     const float streams_work = 3.f * (float)p.all_tiles;
     const int32_t wgs = p.all_tiles ? a.both_wgs : a.wgs;
     // 2^-10 below: the roundings of the sum
@@ -691,7 +705,8 @@ struct Item {
   Parts parts;
 };
 
-__device__ __forceinline__ void find_item(const AttendArgs& a, const Lengths& n, const Plan& p, Item& it, uint32_t id, int tid) {
+__device__ __forceinline__ void find_item(const AttendArgs& a, const Lengths& n, const Plan& p, Item& it, uint32_t id,
+                                          int tid) {
   if (tid == 0) it.valid = 0;
   __syncthreads();
   uint32_t at = p.items, u = p.units;
@@ -779,7 +794,8 @@ __device__ __forceinline__ void attend_streams(const AttendArgs& a, const Length
 
   const uint16_t *ctx_k = kept(a.ctx_k), *ctx_v = kept(a.ctx_v), *page_k = kept(a.k_pages), *page_v = kept(a.v_pages);
   const int32_t max_ctx = kept(a.max_ctx);
-  const int64_t ctx_row = kept(layer * a.n_groups * (int64_t)a.max_ctx), page_row0 = kept((layer * a.n_pages) << a.page_shift);
+  const int64_t ctx_row = kept(layer * a.n_groups * (int64_t)a.max_ctx);
+  const int64_t page_row0 = kept((layer * a.n_pages) << a.page_shift);
 
   for (uint32_t from = 0;;) {
     if (tid < 3) n_seg[tid] = 0;
@@ -901,8 +917,8 @@ __device__ __forceinline__ void attend_streams(const AttendArgs& a, const Length
           load(u, find(u));
           const int32_t rows = rows_of(u);
           stage_k(rows);
-          attend_rows<PARTS, true>(tile, pv, qf, u.tile < u.nctx ? rows : min(rows, limit - (u.tile - u.nctx) * kStreamRows),
-                                   a.scale2, lane, st, [] {});
+          const int32_t left = u.tile < u.nctx ? rows : min(rows, limit - (u.tile - u.nctx) * kStreamRows);
+          attend_rows<PARTS, true>(tile, pv, qf, left, a.scale2, lane, st, [] {});
         }
         if (l.s < ns) load(l, find(l));           // the next piece's first tile again
       }
@@ -969,12 +985,13 @@ struct StageReads {
   }
 };
 
-// The rows of N stages into the state; a column sees the first left(u) of them (whole: all of all).  Two
-// at once make one decision about the maximum for 64 rows, and the second tile's scores are formed while
+// The rows of N stages, tiles t and t + 1, into the state; a column sees the first left(tile) of them (whole: all of
+// both).  Two at once make one decision about the maximum for 64 rows, and the second tile's scores are formed while
 // the first one's settle.  kf: the K fragments of a single tile where they have been read already.
 template <int PARTS, bool CAREFUL, int N, typename Left>
-__device__ __forceinline__ void attend_tiles(const u32x4* kf, const u32x4* stage_a, const u32x4* stage_b, const StageReads& at, const u32x4* qf,
-                                             bool whole, Left&& left, float scale2, int h, State& st) {
+__device__ __forceinline__ void attend_tiles(const u32x4* kf, const u32x4* stage_a, const u32x4* stage_b,
+                                             const StageReads& at, const u32x4* qf, int32_t t, bool whole, Left&& left,
+                                             float scale2, int h, State& st) {
   f32x16 s[N];
 #pragma unroll
   for (int u = 0; u < N; ++u) {
@@ -991,8 +1008,8 @@ __device__ __forceinline__ void attend_tiles(const u32x4* kf, const u32x4* stage
   }
   if (!whole) {
     asm volatile("" ::: );      // a branch: most tiles are whole, and selects for all would cost what the exps do
-    mask_rows(s[0], left(0), h);
-    if (N == 2) mask_rows(s[N - 1], left(1), h);
+    mask_rows(s[0], left(t), h);
+    if (N == 2) mask_rows(s[N - 1], left(t + 1), h);
   }
   float top = max16(s[0]);
   if (N == 2) top = fmaxf(top, max16(s[N - 1]));
@@ -1066,9 +1083,9 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
   wg_most = uni(wg_most);
   tile1 = min(tile1, nctx + (wg_most + kTileRows - 1) / kTileRows);
 
-  // This wave's loads: rows 8 wave + 4 i + (lane >> 4) of K and of V.  The tiles' rows are found by waves: 8
-  // memory rows follow each other, and so do 8 local rows of a page, so one row number and fixed lane offsets address a wave's loads of a whole tile.  Partial
-  // tiles, and local rows that do not lie in eights (small pages, an odd start), are found row by row.
+  // This wave's loads: rows 8 wave + 4 i + (lane >> 4) of K and of V.  8 memory rows follow each other, and so do 8
+  // local rows of a page, so one row number and fixed lane offsets address a wave's loads of a whole tile.
+  // Partial tiles, and local rows that do not lie in eights (small pages, an odd start), are found row by row.
   constexpr int kPer = kTileRows / 4 / kWaves;
   const int64_t ctx_at = (layer * a.n_groups + uni(x.grp)) * (int64_t)a.max_ctx * kRow + head * kDim;
   const int64_t page_at = ((layer * a.n_pages) << a.page_shift) * kRow + head * kDim;
@@ -1131,9 +1148,9 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
   const StageReads at(lane);
   State st;
   clear(st);
-  // rows of tile t that a column sees, or more; rows that all the wave's columns see
+  // rows of tile t that a column sees, or more; whether all the wave's columns see all of it
   auto left_of = [&](int32_t t) __attribute__((always_inline)) {
-    return t < nctx ? jc - t * kTileRows : limit - (t - nctx) * kTileRows;
+    return t >= tile1 ? 0 : (t < nctx ? jc - t * kTileRows : limit - (t - nctx) * kTileRows);
   };
   auto whole = [&](int32_t t) __attribute__((always_inline)) {
     return t != odd && t < whole_end;
@@ -1155,7 +1172,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
       issue(t + 3, page_a, before);
       find(min(t + 4, last), page_a);
     }
-    attend_tiles<PARTS, false, 1>(kf, stage, stage, at, qf, whole(t), [&](int) __attribute__((always_inline)) { return left_of(t); }, a.scale2, h, st);
+    attend_tiles<PARTS, false, 1>(kf, stage, stage, at, qf, t, whole(t), left_of, a.scale2, h, st);
   };
   // Fewer blocks, bound by the rows' bytes: four tiles a step, one or two for each wave, and the next four only
   // once all are done: the other workgroup of the CU computes or loads meanwhile.  (Two tiles in use and two on
@@ -1182,9 +1199,8 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
       asm volatile("s_barrier" ::: "memory");
       const int32_t u = t + N * turn;
       if (u < tile1)
-        attend_tiles<PARTS, false, N>(nullptr, sa, sb, at, qf, u + N - 1 < tile1 && whole(u) && whole(u + N - 1), [&](int v) __attribute__((always_inline)) {
-          return u + v < tile1 ? left_of(u + v) : 0;
-        }, a.scale2, h, st);
+        attend_tiles<PARTS, false, N>(nullptr, sa, sb, at, qf, u, u + N - 1 < tile1 && whole(u) && whole(u + N - 1),
+                                      left_of, a.scale2, h, st);
       if (t + kWaves >= tile1) break;
       asm volatile("s_barrier" ::: "memory");
       issue_all(t + kWaves);
@@ -1224,7 +1240,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
       __builtin_amdgcn_s_waitcnt(kWaitAll);
       __syncthreads();
       if ((t & (share - 1)) == turn)
-        attend_tiles<PARTS, true, 1>(nullptr, stage0, stage0, at, qf, false, [&](int) __attribute__((always_inline)) { return left_of(t); }, a.scale2, h, st);
+        attend_tiles<PARTS, true, 1>(nullptr, stage0, stage0, at, qf, t, false, left_of, a.scale2, h, st);
       __syncthreads();
     }
   }
@@ -1280,7 +1296,8 @@ attend_kernel(const AttendArgs a) {
   load_lengths(a, n, layer, tid);
   const Plan p = make_plan(a, n, tid);
   const uint32_t id = blockIdx.z * gridDim.y + blockIdx.y;
-  // items that fit the chip at once are the longer ones; items of many rounds end more evenly than shares
+  // items that fit the chip at once are the longer ones (16 samples of one question: 173 us, shares first 179);
+  // items of many rounds end more evenly than shares
   const bool items_first = p.all_items <= (uint32_t)a.both_wgs;
   const uint32_t first_share = items_first ? p.all_items : 0, first_item = items_first ? 0 : p.shares;
   if (id >= first_share && id < first_share + p.shares) {      // uniform
@@ -1369,8 +1386,8 @@ attend_join_kernel(const AttendArgs a, int32_t per) {
   }
 }
 
-// Bounds for one layer.  Shares: the workgroups aimed at, one more next to items.  Streamed pieces: one for each share and one
-// more for each stream.  An item job of n > 16 columns has 8 ceil(n / 128) items a chunk, at most n / 2
+// Bounds for one layer.  Shares: the workgroups aimed at, one more next to items.  Streamed pieces: one for each
+// share and one more for each stream.  An item job of n > 16 columns has 8 ceil(n / 128) items a chunk, at most n / 2
 // (8 at 17, 16 at 129) and 8 + n / 16; the items of jobs cut into more chunks and the shares are together
 // at most the workgroups aimed at, and one.  Parts come from all items in groups, else only from jobs
 // that are cut.
@@ -1427,8 +1444,8 @@ hipError_t launch_attend(int32_t L, int32_t B, int32_t n_groups, int32_t n_q, in
                          void* ws, hipStream_t s) {
   const Sizes z = sizes_of(L, B, n_groups, n_q, Hq / kHeads);
   char* w = static_cast<char*>(ws);
-  const AttendArgs a = {B, n_groups, n_q, Hq, Hq / kHeads, __builtin_ctz(Hq / kHeads), max_ctx, n_pages, page_shift, max_pages, q, q_off, grp_off,
-                        ctx_k, ctx_v, ctx_len, k_pages, v_pages, page_table, kv_len, pre_len,
+  const AttendArgs a = {B, n_groups, n_q, Hq, Hq / kHeads, __builtin_ctz(Hq / kHeads), max_ctx, n_pages, page_shift,
+                        max_pages, q, q_off, grp_off, ctx_k, ctx_v, ctx_len, k_pages, v_pages, page_table, kv_len, pre_len,
                         scale * 1.4426950408889634f, out, z.wgs, z.both_wgs, z.unit_cols, z.stream_units, z.max_units,
                         reinterpret_cast<int4*>(w), reinterpret_cast<float2*>(w + z.desc),
                         reinterpret_cast<float*>(w + z.desc + z.ml)};
