@@ -10,8 +10,9 @@
 // tokens, or alone in its group, makes one job over everything; the others of a group make one job of
 // all their tokens over the shared rows and one job each over its own rows.  Memory rows are visible to
 // all columns of a job; of the local rows a column sees those below its own limit.  Lengths are on the
-// device, so each workgroup forms the list itself (a few loads and two scans over the jobs, in LDS)
-// and finds its part of it; the host only bounds the number of workgroups.
+// device, so each workgroup forms the list itself (a few loads and two scans over the jobs, in LDS; calls of
+// many workgroups do so once, attend_plan_kernel) and finds its part of it; the host only bounds the number
+// of workgroups.
 //
 // One kernel (attend_kernel) whose workgroups are of two kinds, so that both fill the chip together:
 // - jobs of up to 16 columns are bound by the rows' bytes: a wave takes one KV head and streams rows
@@ -67,6 +68,12 @@ constexpr int kSegments = 32;             // pieces of streams a workgroup lists
 // 173 with 56, 186 with 64, 182 with 72.
 constexpr int kWgs = 512;
 constexpr int kBothWgs = 56;
+// A call of more workgroups than this has its plans made once, in a launch before: 2,048 sequences of 16 rows behind
+// 64 that each eight share, 18 layers, take 4.1 ms (14.3 with a plan in every workgroup); one token over 4,364
+// rows would take 66 us, so 62.
+constexpr int64_t kPlanWgs = 4096;
+
+struct Plan;
 
 struct AttendArgs {
   int32_t B, n_groups, n_q, Hq, G, g_shift, max_ctx, n_pages, page_shift, max_pages;
@@ -84,6 +91,7 @@ struct AttendArgs {
   int4* desc;                             // [L][n_q][own rows, shared rows][2]: where a token's parts are
   float2* ml;                             // [L][max_units][unit_cols]: maximum (log2 units) and sum
   float* acc;                             // [L][max_units][unit_cols][128]
+  Plan* plans;                            // [L][kThreads], or null: each workgroup makes its own
 };
 
 struct Job {
@@ -631,6 +639,11 @@ __device__ __forceinline__ Plan make_plan(const AttendArgs& a, const Lengths& n,
   return p;
 }
 
+// This thread's part of the layer's plan, from the launch before or made here.
+__device__ __forceinline__ Plan plan_of(const AttendArgs& a, const Lengths& n, int64_t layer, int tid) {
+  return a.plans ? a.plans[layer * kThreads + tid] : make_plan(a, n, tid);
+}
+
 struct Segment {
   Job x;
   int32_t set, tile0, tile1;    // head set, tiles of the stream
@@ -933,7 +946,7 @@ __device__ __forceinline__ void attend_streams(const AttendArgs& a, const Length
     from = reached;
     __syncthreads();
     load_lengths(a, n, layer, tid);
-    p = make_plan(a, n, tid);
+    p = plan_of(a, n, layer, tid);
   }
 }
 
@@ -1292,10 +1305,11 @@ attend_kernel(const AttendArgs a) {
   const int tid = threadIdx.x;
   // layers fastest: the workgroups that turn out to have nothing to do come last
   const int64_t layer = blockIdx.x;
+  const uint32_t id = blockIdx.z * gridDim.y + blockIdx.y;
+  if (a.plans && id >= a.plans[layer * kThreads].shares + a.plans[layer * kThreads].all_items) return;
   const Lengths n = lengths_in(stage0, stage1, stage2, stage3);
   load_lengths(a, n, layer, tid);
-  const Plan p = make_plan(a, n, tid);
-  const uint32_t id = blockIdx.z * gridDim.y + blockIdx.y;
+  const Plan p = plan_of(a, n, layer, tid);
   // items that fit the chip at once are the longer ones (16 samples of one question: 173 us, shares first 179);
   // items of many rounds end more evenly than shares
   const bool items_first = p.all_items <= (uint32_t)a.both_wgs;
@@ -1309,6 +1323,15 @@ attend_kernel(const AttendArgs a) {
     find_item(a, n, p, sh.item.item, id - first_item, tid);
     if (sh.item.item.valid) attend_item<BF16_OUT>(a, n, sh.item, stage0, stage1, stage2, stage3, layer, tid);
   }
+}
+
+// The plans of all layers.
+__global__ void __launch_bounds__(kThreads)
+attend_plan_kernel(const AttendArgs a) {
+  __shared__ u32x4 s0[kStage], s1[kStage], s2[kStage], s3[kStage];
+  const Lengths n = lengths_in(s0, s1, s2, s3);
+  load_lengths(a, n, blockIdx.x, threadIdx.x);
+  a.plans[blockIdx.x * (int64_t)kThreads + threadIdx.x] = make_plan(a, n, threadIdx.x);
 }
 
 // Joins the parts of a token's own rows and of its group's shared rows: four dims of one query head
@@ -1393,7 +1416,7 @@ attend_join_kernel(const AttendArgs a, int32_t per) {
 // that are cut.
 struct Sizes {
   int32_t wgs, both_wgs, grid, unit_cols, stream_units, max_units;
-  size_t desc, ml, acc, total;
+  size_t desc, ml, acc, plans, total;
 };
 
 Sizes sizes_of(int64_t L, int64_t B, int64_t n_groups, int64_t n_q, int64_t G) {
@@ -1415,7 +1438,8 @@ Sizes sizes_of(int64_t L, int64_t B, int64_t n_groups, int64_t n_q, int64_t G) {
   z.desc = up((size_t)L * n_q * 4 * sizeof(int4));
   z.ml = up((size_t)L * z.max_units * z.unit_cols * sizeof(float2));
   z.acc = up((size_t)L * z.max_units * z.unit_cols * kDim * sizeof(float));
-  z.total = z.desc + z.ml + z.acc;
+  z.plans = L * z.grid > kPlanWgs ? up((size_t)L * kThreads * sizeof(Plan)) : 0;
+  z.total = z.desc + z.ml + z.acc + z.plans;
   return z;
 }
 
@@ -1427,6 +1451,7 @@ size_t attend_workspace_bytes(int32_t L, int32_t B, int32_t n_groups, int32_t n_
 
 template <bool BF16_OUT>
 static void launch_attend_as(const AttendArgs& a, const Sizes& z, int32_t L, hipStream_t s) {
+  if (a.plans) hipLaunchKernelGGL(attend_plan_kernel, dim3((unsigned)L), dim3(kThreads), 0, s, a);
   const unsigned most = 32768, y = (unsigned)z.grid < most ? (unsigned)z.grid : most;    // a launch's y may have 65,535
   hipLaunchKernelGGL(attend_kernel<BF16_OUT>, dim3((unsigned)L, y, (z.grid + y - 1) / y), dim3(kThreads), 0, s, a);
   // a workgroup for 8 heads of one token, of several (at most 64) where there are many
@@ -1448,7 +1473,8 @@ hipError_t launch_attend(int32_t L, int32_t B, int32_t n_groups, int32_t n_q, in
                         max_pages, q, q_off, grp_off, ctx_k, ctx_v, ctx_len, k_pages, v_pages, page_table, kv_len, pre_len,
                         scale * 1.4426950408889634f, out, z.wgs, z.both_wgs, z.unit_cols, z.stream_units, z.max_units,
                         reinterpret_cast<int4*>(w), reinterpret_cast<float2*>(w + z.desc),
-                        reinterpret_cast<float*>(w + z.desc + z.ml)};
+                        reinterpret_cast<float*>(w + z.desc + z.ml),
+                        z.plans ? reinterpret_cast<Plan*>(w + z.desc + z.ml + z.acc) : nullptr};
   if (bf16_out) launch_attend_as<true>(a, z, L, s);
   else launch_attend_as<false>(a, z, L, s);
   return hipGetLastError();
