@@ -22,10 +22,10 @@
 // attend_join_kernel joins where a column's rows were cut into parts; what is whole in one part has been
 // written by the workgroup that computed it.  (A workgroup that joins for the others would need a counter and
 // a device-wide release in each; the launch costs ~5 us.)
-// Measured: one token of 32 heads over 4,364 rows in 18 layers 61 us (4.9 TB/s); a prompt of 8,000 tokens
-// over 4,300 memory rows 1.03-1.12 ms (960-1,044 TFLOP/s, bf16 output), matrix cores 41% busy and vector units 43%, which
-// overlap little; each scalar or vector instruction between a tile's barrier and its last product
-// still shows in the time.
+// Measured: one token of 32 heads over 4,364 rows in 18 layers 61 us (4.9 TB/s); a prompt of 8,000 tokens over 4,300
+// memory rows 1.03-1.10 ms (980-1,044 TFLOP/s, bf16 output).  There the matrix cores are 50% busy and the
+// vector units 44%; they overlap little, every instruction between a tile's barrier and its last product
+// shows in the time, and the clock gives way as the work gets denser (2.16 GHz at 1.18 ms, 1.94 at 1.07).
 // In both, S^T = K . Q^T is computed with K as the A operand and the columns as the B operand
 // (registers), so a lane holds scores of one column and the softmax needs only exchanges between the
 // lane groups of a wave; for O^T += V^T . P^T the MFMA's k axis is taken in the order in which the scores
