@@ -399,7 +399,7 @@ int msa_paged_append(int32_t n_layers, int32_t B, int32_t n_q, int32_t Hq, const
  *   ctx_k, ctx_v  [n_layers][n_groups][max_ctx][8][128] bf16 (as msa_gather_ctx writes them for
  *                 n_groups queries); ctx_len [n_layers][n_groups] int32.  NULL when max_ctx == 0
  *   pre_len       [n_groups] int32 or NULL
- *   scale         positive and finite
+ *   scale         positive, below 2.3e38
  *   out           [n_layers][n_q][Hq][128], fp32 (out_bf16 = 0) or bf16 (out_bf16 = 1); zero for
  *                 a token that sees no row
  *

@@ -515,8 +515,8 @@ MSA_API int msa_paged_attend(int32_t n_layers, int32_t B, int32_t n_groups, int3
     return fail(MSA_ERR_SHAPE, "msa_paged_attend: n_groups=%d B=%d max_ctx=%d", n_groups, B, max_ctx);
   if (n_groups < B && !grp_off) return fail(MSA_ERR_NULL, "msa_paged_attend: null grp_off");
   if (max_ctx > MSA_MAX_LOCAL_ROWS) return fail(MSA_ERR_UNSUPPORTED, "msa_paged_attend: max_ctx=%d", max_ctx);
-  if (!(scale > 0.f) || !(scale < __builtin_inff()))
-    return fail(MSA_ERR_SHAPE, "msa_paged_attend: scale=%g must be positive and finite", (double)scale);
+  if (!(scale > 0.f) || !(scale * 1.4426950408889634f < __builtin_inff()))     // the kernel's scores are in log2 units
+    return fail(MSA_ERR_SHAPE, "msa_paged_attend: scale=%g must be positive and below 2.3e38", (double)scale);
   if (out_bf16 != 0 && out_bf16 != 1) return fail(MSA_ERR_SHAPE, "msa_paged_attend: out_bf16=%d", out_bf16);
   const size_t need = msa_paged_attend_workspace_size(n_layers, B, n_groups, n_q, Hq);
   if (workspace_bytes < need)

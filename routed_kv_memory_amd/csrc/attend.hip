@@ -1360,7 +1360,7 @@ attend_join_kernel(const AttendArgs a, int32_t per) {
       if (which == 0) last = d1.w != 0;
       const int32_t unit = first + (head % kWaves) * d1.x;
       // holds for every token of a sequence; offsets that are not ascending may leave a token without parts
-      if (first < 0 || n < 1 || d1.x < 0 || d1.x > kWaves || d1.y < 0 || col < 0 || col >= a.unit_cols ||
+      if (first < 0 || n < 1 || n > a.max_units || d1.x < 0 || d1.x > kWaves || d1.y < 0 || col < 0 || col >= a.unit_cols ||
           unit + (int64_t)(n - 1) * d1.y >= a.max_units) {
         ok = false;
         break;

@@ -133,3 +133,8 @@ def test_attend_binding_refuses(msa, change, error):
     with pytest.raises(error):
         msa.msa_paged_attend(a["q"], a["q_off"], a["kv_len"], a["page_table"], a["k_pages"], a["v_pages"], 0.1, out,
                              torch.zeros(8, dtype=torch.uint8), **change)
+
+
+def test_attend_refuses_a_scale_past_the_range_of_its_scores(msa):
+    assert attend(msa, scale=F(2.4e38)) == SHAPE
+    assert attend(msa, scale=F(3.4e38)) == SHAPE
