@@ -1336,76 +1336,93 @@ attend_plan_kernel(const AttendArgs a) {
 
 // Joins the parts of a token's own rows and of its group's shared rows: four dims of one query head
 // a thread, the parts in order with a running maximum.
-// A workgroup takes 8 heads of `per` tokens, of which it first looks up which have parts at all.
+// A workgroup takes 8 heads of `per` tokens, of which it first looks up which have parts at all.  Latency is all
+// here: the first token's descriptors are asked for at once with that, and own and shared parts together.
 template <bool BF16_OUT>
 __global__ void __launch_bounds__(256)
 attend_join_kernel(const AttendArgs a, int32_t per) {
   const int64_t layer = blockIdx.z;
-  const int32_t t0 = blockIdx.x * per, tn = min(t0 + per, clampi(a.q_off[a.B], 0, a.n_q));
+  const int32_t t0 = blockIdx.x * per;
   const int lane = threadIdx.x & 63;
   const int32_t hq = blockIdx.y * 8 + (threadIdx.x >> 5), d4 = 4 * (threadIdx.x & 31);
   const int32_t head = hq / a.G, hh = hq % a.G, set = head / kWaves;
   const int4* descs = a.desc + layer * a.n_q * 4;
+  int4 d[4];                                // own rows' descriptor, the shared rows'
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = descs[(int64_t)t0 * 4 + i];
+  const int32_t first_unit = descs[(int64_t)min(t0 + lane, a.n_q - 1) * 4].x;
+  const int32_t tn = min(t0 + per, clampi(a.q_off[a.B], 0, a.n_q));
   // per <= 64; a token whose first set has parts has parts of every set
-  uint64_t todo = __ballot(t0 + lane < tn && descs[(int64_t)(t0 + lane) * 4].x >= 0);
+  uint64_t todo = __ballot(t0 + lane < tn && first_unit >= 0);
   for (; todo; todo &= todo - 1) {
     const int32_t t = t0 + __builtin_ctzll(todo);
-    const int4* desc = descs + (int64_t)t * 4;
-    float m = -__builtin_huge_valf(), l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t != t0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] = descs[(int64_t)t * 4 + i];
+    }
+    // parts 0 .. n[0] are the own rows', from there to n[0] + n[1] the shared rows'
+    int32_t n[2];
+    int64_t at[2], step[2];
     bool ok = true;
-    for (int which = 0, last = 0; which <= last; ++which) {
-      const int4 d0 = desc[2 * which], d1 = desc[2 * which + 1];
-      const int32_t first = set ? d0.z : d0.x, n = set ? d0.w : d0.y, col = d1.z + hh;
-      if (which == 0) last = d1.w != 0;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const int4 d0 = d[2 * which], d1 = d[2 * which + 1];
+      n[which] = 0;
+      at[which] = step[which] = 0;
+      if (which == 1 && d[1].w == 0) continue;
+      const int32_t first = set ? d0.z : d0.x, parts = set ? d0.w : d0.y, col = d1.z + hh;
       const int32_t unit = first + (head % kWaves) * d1.x;
       // holds for every token of a sequence; offsets that are not ascending may leave a token without parts
-      if (first < 0 || n < 1 || n > a.max_units || d1.x < 0 || d1.x > kWaves || d1.y < 0 || col < 0 || col >= a.unit_cols ||
-          unit + (int64_t)(n - 1) * d1.y >= a.max_units) {
-        ok = false;
-        break;
-      }
-      const int64_t at = (layer * a.max_units + unit) * a.unit_cols + col, step = (int64_t)d1.y * a.unit_cols;
-      for (int32_t k0 = 0; k0 < n; k0 += 8) {
-        float2 ml[8];
-        float4 v[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int64_t p = at + min(k0 + u, n - 1) * step;
-          ml[u] = a.ml[p];
-          v[u] = *reinterpret_cast<const float4*>(a.acc + p * kDim + d4);
-        }
-        float mn = m;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) mn = fmaxf(mn, ml[u].x);
-        const float base = mn == -__builtin_huge_valf() ? 0.f : mn;     // no row so far
-        const float s = __builtin_amdgcn_exp2f(m - base);
-        l *= s;
-        o.x *= s;
-        o.y *= s;
-        o.z *= s;
-        o.w *= s;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          if (k0 + u >= n) continue;
-          const float w = __builtin_amdgcn_exp2f(ml[u].x - base);
-          l += w * ml[u].y;
-          o.x += w * v[u].x;
-          o.y += w * v[u].y;
-          o.z += w * v[u].z;
-          o.w += w * v[u].w;
-        }
-        m = mn;
-      }
+      ok &= first >= 0 && parts >= 1 && parts <= a.max_units && d1.x >= 0 && d1.x <= kWaves && d1.y >= 0 && col >= 0 &&
+            col < a.unit_cols && unit + (int64_t)(parts - 1) * d1.y < a.max_units;
+      n[which] = parts;
+      at[which] = (layer * a.max_units + unit) * a.unit_cols + col;
+      step[which] = (int64_t)d1.y * a.unit_cols;
     }
     if (!ok) continue;
+    const int32_t all = n[0] + n[1];
+    float m = -__builtin_huge_valf(), l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < all; k0 += 8) {
+      float2 ml[8];
+      float4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int32_t k = min(k0 + u, all - 1);
+        const int64_t p = k < n[0] ? at[0] + k * step[0] : at[1] + (k - n[0]) * step[1];
+        ml[u] = a.ml[p];
+        v[u] = *reinterpret_cast<const float4*>(a.acc + p * kDim + d4);
+      }
+      float mn = m;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) mn = fmaxf(mn, ml[u].x);
+      const float base = mn == -__builtin_huge_valf() ? 0.f : mn;     // no row so far
+      const float s = __builtin_amdgcn_exp2f(m - base);
+      l *= s;
+      o.x *= s;
+      o.y *= s;
+      o.z *= s;
+      o.w *= s;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (k0 + u >= all) continue;
+        const float w = __builtin_amdgcn_exp2f(ml[u].x - base);
+        l += w * ml[u].y;
+        o.x += w * v[u].x;
+        o.y += w * v[u].y;
+        o.z += w * v[u].z;
+        o.w += w * v[u].w;
+      }
+      m = mn;
+    }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t at = ((layer * a.n_q + t) * a.Hq + hq) * kDim + d4;
+    const int64_t row = ((layer * a.n_q + t) * a.Hq + hq) * kDim + d4;
     if (BF16_OUT)
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row) =
           make_uint2(pack2_bf16(o.x * inv, o.y * inv), pack2_bf16(o.z * inv, o.w * inv));
     else
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row) =
+          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   }
 }
 
