@@ -308,11 +308,19 @@ def _dims(t, n, name):
     return t.shape
 
 
-def _on(dev, t, dtypes, shape, name):
-    """Address of a contiguous tensor of this shape on GPU `dev` (the kernels take the sizes from other
-    arguments); None for none."""
+def _on(dev, t, dtypes, shape, name, have=None):
+    """Address of a contiguous tensor of this shape (None: any; `have`: its shape, where it is known) on GPU
+    `dev` (the kernels take the sizes from other arguments); None for none."""
     if t is None:
         return None
+    if isinstance(t, torch.Tensor):
+        if ((shape is None or (have or t.shape) == shape) and t.dtype in dtypes and t.is_contiguous()
+                and t.get_device() == dev and dev >= 0):
+            return t.data_ptr()
+    _refuse(dev, t, dtypes, shape, name)
+
+
+def _refuse(dev, t, dtypes, shape, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if shape is not None and t.shape != shape:
@@ -321,12 +329,9 @@ def _on(dev, t, dtypes, shape, name):
         raise TypeError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtypes))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    d = t.get_device()
-    if d != dev or d < 0:
-        if not t.is_cuda:
-            raise ValueError("%s must be a GPU tensor" % name)
-        raise ValueError("%s is on cuda:%d, the other tensors on cuda:%d" % (name, d, dev))
-    return t.data_ptr()
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % name)
+    raise ValueError("%s is on cuda:%d, the other tensors on cuda:%d" % (name, t.get_device(), dev))
 
 
 def _required(**tensors):
@@ -358,25 +363,27 @@ def msa_paged_append(k_new, v_new, q, q_off, kv_len, page_table, k_pages, v_page
     """k_new, v_new [L][n_q][8][128], q and q_out [L][n_q][Hq][128] (q may be None, q_out may be q);
     q_off [B+1], kv_len [B] (new tokens included), page_table [B][max_pages], pos_off [B] int32;
     k_pages, v_pages [L][n_pages][page_tokens][8][128]; w_k, w_q [L][128] or None (no norm)."""
-    L, n_q = _dims(k_new, 4, "k_new")[:2]
-    pages = _dims(k_pages, 5, "k_pages")
-    n_pages, page_tokens = pages[1], pages[2]
+    k_shape = _dims(k_new, 4, "k_new")
+    L, n_q = k_shape[0], k_shape[1]
+    p_shape = _dims(k_pages, 5, "k_pages")
+    n_pages, page_tokens = p_shape[1], p_shape[2]
     B, max_pages = _dims(page_table, 2, "page_table")
     _required(v_new=v_new, q_off=q_off, kv_len=kv_len, v_pages=v_pages)
     if q is None:
-        Hq, q_out, w_q = 0, None, None
+        Hq, q_out, w_q, q_shape = 0, None, None, None
     else:
-        Hq = _dims(q, 4, "q")[2]
+        q_shape = _dims(q, 4, "q")
+        Hq = q_shape[2]
         _required(q_out=q_out)
     dev = k_new.get_device()
     new, pages, heads = (L, n_q, HEADS, HEAD_DIM), (L, n_pages, page_tokens, HEADS, HEAD_DIM), (L, n_q, Hq, HEAD_DIM)
     _call("msa_paged_append", dev, stream, (
-        L, B, n_q, Hq, _on(dev, k_new, _BF16, new, "k_new"), _on(dev, v_new, _BF16, new, "v_new"),
-        _on(dev, q, _BF16, heads, "q"), _on(dev, q_off, _I32T, (B + 1,), "q_off"),
+        L, B, n_q, Hq, _on(dev, k_new, _BF16, new, "k_new", k_shape), _on(dev, v_new, _BF16, new, "v_new"),
+        _on(dev, q, _BF16, heads, "q", q_shape), _on(dev, q_off, _I32T, (B + 1,), "q_off"),
         _on(dev, kv_len, _I32T, (B,), "kv_len"), _on(dev, pos_off, _I32T, (B,), "pos_off"),
         _on(dev, page_table, _I32T, None, "page_table"), max_pages, page_tokens, n_pages,
         _on(dev, w_k, _BF16, (L, HEAD_DIM), "w_k"), _on(dev, w_q, _BF16, (L, HEAD_DIM), "w_q"), float(eps),
-        float(theta), _on(dev, k_pages, _BF16, pages, "k_pages"), _on(dev, v_pages, _BF16, pages, "v_pages"),
+        float(theta), _on(dev, k_pages, _BF16, pages, "k_pages", p_shape), _on(dev, v_pages, _BF16, pages, "v_pages"),
         _on(dev, q_out, _BF16, heads, "q_out")))
 
 
@@ -389,12 +396,12 @@ def msa_paged_attend(q, q_off, kv_len, page_table, k_pages, v_pages, scale, out,
     """q [L][n_q][Hq][128]; the cache as for msa_paged_append; grp_off [n_groups+1] (None: every
     sequence its own group), ctx_k, ctx_v [L][n_groups][max_ctx][8][128] and ctx_len [L][n_groups]
     (None: no memory context), pre_len [n_groups] or None; out [L][n_q][Hq][128], fp32 or bf16."""
-    heads = _dims(q, 4, "q")
-    L, n_q, Hq = heads[0], heads[1], heads[2]
-    pages = _dims(k_pages, 5, "k_pages")
-    n_pages, page_tokens = pages[1], pages[2]
+    q_shape = _dims(q, 4, "q")
+    L, n_q, Hq = q_shape[0], q_shape[1], q_shape[2]
+    p_shape = _dims(k_pages, 5, "k_pages")
+    n_pages, page_tokens = p_shape[1], p_shape[2]
     B, max_pages = _dims(page_table, 2, "page_table")
-    _dims(out, 4, "out")
+    o_shape = _dims(out, 4, "out")
     _required(q_off=q_off, kv_len=kv_len, v_pages=v_pages, workspace=workspace)
     n_groups = B if grp_off is None else _dims(grp_off, 1, "grp_off")[0] - 1
     if ctx_k is None:
@@ -406,11 +413,12 @@ def msa_paged_attend(q, q_off, kv_len, page_table, k_pages, v_pages, scale, out,
     heads, pages = (L, n_q, Hq, HEAD_DIM), (L, n_pages, page_tokens, HEADS, HEAD_DIM)
     ctx = (L, n_groups, max_ctx, HEADS, HEAD_DIM)
     _call("msa_paged_attend", dev, stream, (
-        L, B, n_groups, n_q, Hq, _on(dev, q, _BF16, heads, "q"), _on(dev, q_off, _I32T, (B + 1,), "q_off"),
+        L, B, n_groups, n_q, Hq, _on(dev, q, _BF16, heads, "q", q_shape), _on(dev, q_off, _I32T, (B + 1,), "q_off"),
         _on(dev, grp_off, _I32T, None, "grp_off"), _on(dev, ctx_k, _BF16, ctx, "ctx_k"),
         _on(dev, ctx_v, _BF16, ctx, "ctx_v"), _on(dev, ctx_len, _I32T, (L, n_groups), "ctx_len"), max_ctx,
-        _on(dev, k_pages, _BF16, pages, "k_pages"), _on(dev, v_pages, _BF16, pages, "v_pages"), n_pages, page_tokens,
+        _on(dev, k_pages, _BF16, pages, "k_pages", p_shape), _on(dev, v_pages, _BF16, pages, "v_pages"), n_pages,
+        page_tokens,
         _on(dev, page_table, _I32T, None, "page_table"), max_pages, _on(dev, kv_len, _I32T, (B,), "kv_len"),
         _on(dev, pre_len, _I32T, (n_groups,), "pre_len"), float(scale), 0 if out.dtype == torch.float32 else 1,
-        _on(dev, out, _F32_BF16, heads, "out"), _on(dev, workspace, _ANY, None, "workspace"),
+        _on(dev, out, _F32_BF16, heads, "out", o_shape), _on(dev, workspace, _ANY, None, "workspace"),
         workspace.numel() * workspace.element_size()))
