@@ -82,3 +82,35 @@ def test_nothing_around_the_buffers_changes(case):
         assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
         live = [s for s in range(b.B) if b.new[s]]
         check_attention(b, outs[0], tokens=[(l, s, b.new[s] - 1) for l in {0, b.L - 1} for s in live[:8] + live[-4:]])
+
+
+def test_captured_call_follows_its_lengths():
+    """A call whose plan is a launch of its own, captured once: each replay sees the lengths of its time."""
+    print("case: captured, many sequences", flush=True)
+    b = Batch([1] * 400, [60 + s % 5 for s in range(400)], groups=[8] * 50, ctx=[[40] * 50] * 6, page=16, hq=32, layers=6,
+              seed=401)
+    d = b.to_device()
+    ws = torch.empty(msa.msa_paged_attend_workspace_size(b.L, b.B, b.G, b.n_q, b.hq), dtype=torch.uint8, device="cuda")
+    out, eager = (torch.zeros(b.L, b.n_q, b.hq, 128, device="cuda") for _ in range(2))
+
+    def call(to):
+        msa.msa_paged_attend(d["q"], d["q_off"], d["kv_len"], d["page_table"], d["k_pages"], d["v_pages"], SCALE, to, ws,
+                             grp_off=d["grp_off"], ctx_k=d["ctx_k"], ctx_v=d["ctx_v"], ctx_len=d["ctx_len"])
+
+    call(eager)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out)
+    gen = torch.Generator().manual_seed(401)
+    for step in range(4):
+        lens = torch.randint(1, 65, (400,), generator=gen, dtype=torch.int32)
+        d["kv_len"].copy_(lens.cuda())
+        d["ctx_len"].copy_(torch.randint(0, 41, (6, 50), generator=gen, dtype=torch.int32).cuda())
+        ws.fill_(step)
+        call(eager)
+        torch.cuda.synchronize()
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager), step
