@@ -655,7 +655,7 @@ struct Segment {
 };
 
 // The pieces of streams in share `number`, from tile `from` of the layer's on: up to kSegments into `seg`, their
-// number in n_seg[0]; returns where the list ends.
+// number in n_seg[0]; returns where the list ends, 0 where that is the share's end.
 __device__ __forceinline__ uint32_t list_segments(const AttendArgs& a, const Lengths& n, const Plan& p, Segment* seg,
                                                   uint32_t* n_seg, uint32_t number, uint32_t from) {
   const uint32_t share = p.share;
@@ -707,7 +707,8 @@ __device__ __forceinline__ uint32_t list_segments(const AttendArgs& a, const Len
     if (k == kSegments - 1) n_seg[2] = min(to, u + t);
   });
   __syncthreads();
-  return n_seg[0] < kSegments ? to : n_seg[2];
+  // a full list may end with the share, also inside a stream
+  return n_seg[0] < kSegments || n_seg[2] >= to ? 0 : n_seg[2];
 }
 
 struct Item {
@@ -942,7 +943,7 @@ __device__ __forceinline__ void attend_streams(const AttendArgs& a, const Length
       const int32_t slot = uni(seg[s].slot);
       write_state<BF16_OUT>(a, st, rows4_sum(st.l), y, layer, slot < 0 ? -1 : kWaves * slot + wave, lane);
     }
-    if (ns < kSegments) return;                   // uniform
+    if (reached == 0) return;                     // uniform
     from = reached;
     __syncthreads();
     load_lengths(a, n, layer, tid);
