@@ -394,8 +394,8 @@ int msa_paged_append(int32_t n_layers, int32_t B, int32_t n_q, int32_t Hq, const
  * mixed in one call.
  *
  *   q             [n_layers][n_q][Hq][128] bf16, Hq in {8, 16, 32, 64}
- *   grp_off       [n_groups + 1] int32, ascending from 0 to B; not read (may be NULL) when
- *                 n_groups == B: then every sequence is its own group
+ *   grp_off       [n_groups + 1] int32, ascending from 0 to B (a group may have no sequence).  NULL
+ *                 (n_groups == B only): every sequence is its own group
  *   ctx_k, ctx_v  [n_layers][n_groups][max_ctx][8][128] bf16 (as msa_gather_ctx writes them for
  *                 n_groups queries); ctx_len [n_layers][n_groups] int32.  NULL when max_ctx == 0
  *   pre_len       [n_groups] int32 or NULL

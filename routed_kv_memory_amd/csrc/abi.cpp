@@ -523,8 +523,8 @@ MSA_API int msa_paged_attend(int32_t n_layers, int32_t B, int32_t n_groups, int3
     return fail(MSA_ERR_WORKSPACE, "msa_paged_attend: workspace %zu < %zu bytes", workspace_bytes, need);
   if (n_q == 0) return MSA_OK;
   void* ws = reinterpret_cast<void*>(align256(reinterpret_cast<size_t>(workspace)));
-  return hip_status(msa::launch_attend(n_layers, B, n_groups, n_q, Hq, q, q_off, n_groups < B ? grp_off : nullptr, ctx_k,
-                                       ctx_v, ctx_len, max_ctx, k_pages, v_pages, n_pages, page_shift_of(page_tokens),
+  return hip_status(msa::launch_attend(n_layers, B, n_groups, n_q, Hq, q, q_off, grp_off, ctx_k, ctx_v, ctx_len,
+                                       max_ctx, k_pages, v_pages, n_pages, page_shift_of(page_tokens),
                                        page_table, max_pages, kv_len, pre_len, scale, out_bf16 == 1, out, ws,
                                        as_stream(stream)),
                     "msa_paged_attend");

@@ -1430,28 +1430,29 @@ attend_join_kernel(const AttendArgs a, int32_t per) {
 // Bounds for one layer.  Shares: the workgroups aimed at, one more next to items.  Streamed pieces: one for each
 // share and one more for each stream.  An item job of n > 16 columns has 8 ceil(n / 128) items a chunk, at most n / 2
 // (8 at 17, 16 at 129) and 8 + n / 16; the items of jobs cut into more chunks and the shares are together
-// at most the workgroups aimed at, and one.  Parts come from all items in groups, else only from jobs
-// that are cut.
+// at most the workgroups aimed at, and one.  Parts come from items of jobs that are cut, and in groups from all items of
+// the shared rows and of the own rows next to them: of sequences of up to kAlone columns, two or more in a run of a
+// group that shares.
 struct Sizes {
   int32_t wgs, both_wgs, grid, unit_cols, stream_units, max_units;
   size_t desc, ml, acc, plans, total;
 };
 
-Sizes sizes_of(int64_t L, int64_t B, int64_t n_groups, int64_t n_q, int64_t G) {
+Sizes sizes_of(int64_t L, int64_t B, int64_t n_groups, int64_t n_q, int64_t G, bool grouped) {
   Sizes z;
-  const bool grouped = n_groups < B;
-  const int64_t cols = n_q * G, all_cols = cols * (grouped ? 2 : 1);
   auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
+  const int64_t cols = n_q * G, shared_cols = grouped ? least(cols, kAlone * B) : 0, all_cols = cols + shared_cols;
   z.wgs = (int32_t)(L < kWgs ? kWgs / L : 1);
   z.both_wgs = z.wgs > kBothWgs ? z.wgs : kBothWgs;
   // every sequence with tokens, and the shared rows of two or more of a group or behind one on its own
-  const int64_t jobs = least(B, n_q) + (grouped ? least(n_groups + cols / kAlone, least(B, n_q)) : 0);
+  const int64_t jobs = least(B, n_q) + (grouped ? least(n_groups + cols / kAlone, least(B / 2, n_q)) : 0);
   const int64_t aimed = cols > kStreamCols ? z.both_wgs + 1 : z.wgs;
   const int64_t whole = cols > kStreamCols ? least(all_cols / 2, kHeads * jobs + all_cols / 16) : 0;
+  const int64_t parts = cols > kStreamCols ? aimed + least(shared_cols, kHeads * jobs + shared_cols / 8) : 0;
   z.grid = (int32_t)(aimed + whole);
   z.unit_cols = (int32_t)least(cols, kCols);
   z.stream_units = (int32_t)(kWaves * (aimed + kSets * jobs));
-  z.max_units = (int32_t)(z.stream_units + (cols > kStreamCols ? kWaves * (aimed + (grouped ? whole : 0)) : 0));
+  z.max_units = (int32_t)(z.stream_units + kWaves * parts);
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   z.desc = up((size_t)L * n_q * 4 * sizeof(int4));
   z.ml = up((size_t)L * z.max_units * z.unit_cols * sizeof(float2));
@@ -1463,8 +1464,12 @@ Sizes sizes_of(int64_t L, int64_t B, int64_t n_groups, int64_t n_q, int64_t G) {
 
 }  // namespace
 
+// Groups cannot share anything between fewer than two sequences.
+static bool can_share(int32_t B) { return B > 1; }
+
+// For a call with groups: one without needs no more, in every term.
 size_t attend_workspace_bytes(int32_t L, int32_t B, int32_t n_groups, int32_t n_q, int32_t Hq) {
-  return sizes_of(L, B, n_groups, n_q, Hq / kHeads).total;
+  return sizes_of(L, B, n_groups, n_q, Hq / kHeads, can_share(B)).total;
 }
 
 template <bool BF16_OUT>
@@ -1485,7 +1490,8 @@ hipError_t launch_attend(int32_t L, int32_t B, int32_t n_groups, int32_t n_q, in
                          int32_t n_pages, int32_t page_shift, const int32_t* page_table, int32_t max_pages,
                          const int32_t* kv_len, const int32_t* pre_len, float scale, bool bf16_out, void* out,
                          void* ws, hipStream_t s) {
-  const Sizes z = sizes_of(L, B, n_groups, n_q, Hq / kHeads);
+  if (!can_share(B)) grp_off = nullptr;      // one sequence, so one group
+  const Sizes z = sizes_of(L, B, n_groups, n_q, Hq / kHeads, grp_off != nullptr);
   char* w = static_cast<char*>(ws);
   const AttendArgs a = {B, n_groups, n_q, Hq, Hq / kHeads, __builtin_ctz(Hq / kHeads), max_ctx, n_pages, page_shift,
                         max_pages, q, q_off, grp_off, ctx_k, ctx_v, ctx_len, k_pages, v_pages, page_table, kv_len, pre_len,

@@ -393,9 +393,10 @@ def msa_paged_attend_workspace_size(n_layers, B, n_groups, n_q, Hq) -> int:
 
 def msa_paged_attend(q, q_off, kv_len, page_table, k_pages, v_pages, scale, out, workspace, grp_off=None, ctx_k=None,
                      ctx_v=None, ctx_len=None, pre_len=None, stream=None):
-    """q [L][n_q][Hq][128]; the cache as for msa_paged_append; grp_off [n_groups+1] (None: every
-    sequence its own group), ctx_k, ctx_v [L][n_groups][max_ctx][8][128] and ctx_len [L][n_groups]
-    (None: no memory context), pre_len [n_groups] or None; out [L][n_q][Hq][128], fp32 or bf16."""
+    """q [L][n_q][Hq][128]; the cache as for msa_paged_append; grp_off [n_groups+1], ascending from 0 to
+    B, n_groups <= B (None: every sequence its own group), ctx_k, ctx_v [L][n_groups][max_ctx][8][128]
+    and ctx_len [L][n_groups] (None: no memory context), pre_len [n_groups] or None; out
+    [L][n_q][Hq][128], fp32 or bf16."""
     q_shape = _dims(q, 4, "q")
     L, n_q, Hq = q_shape[0], q_shape[1], q_shape[2]
     p_shape = _dims(k_pages, 5, "k_pages")
