@@ -53,6 +53,7 @@ constexpr int kCols = 32;                 // columns of a wave that shares tiles
 // one token over 1,500 shared rows: 195 us, 256 us sharing; from 128 to 512 it is the same).
 constexpr int kAlone = 512;
 constexpr int kWide = kWaves * kCols;     // columns of a workgroup of the second kind
+constexpr int kBlockUnits = kCols / kStreamCols;    // units of the workspace that its waves' columns take
 constexpr int kSets = kHeads / kWaves;    // head sets of a streamed job: streams of rows it makes
 constexpr int kStreamRows = 32;           // rows of a streamed tile
 constexpr int kTileRows = 32;             // rows of a shared tile
@@ -86,10 +87,10 @@ struct AttendArgs {
   float scale2;                           // scale * log2 e
   void* out;
   int32_t wgs, both_wgs;                  // workgroups aimed at in a layer: jobs of one kind, of both
-  int32_t unit_cols;                      // columns of a part in the workspace
-  int32_t stream_units, max_units;        // parts of one layer: streamed ones, all
+  int32_t unit_cols;                      // columns of a unit of the workspace: kStreamCols, or fewer if there are no more
+  int32_t stream_units, max_units;        // units of one layer: of streamed parts, all
   int4* desc;                             // [L][n_q][own rows, shared rows][2]: where a token's parts are
-  float2* ml;                             // [L][max_units][unit_cols]: maximum (log2 units) and sum
+  float2* ml;                             // [L][max_units][unit_cols], the parts: maximum (log2 units) and sum
   float* acc;                             // [L][max_units][unit_cols][128]
   Plan* plans;                            // [L][kThreads], or null: each workgroup makes its own
 };
@@ -527,7 +528,7 @@ __device__ __forceinline__ void write_state(const AttendArgs& a, const State16& 
 
 // Where a token's parts are: part k of head h of a column is unit
 //   first[h / kWaves] + (h % kWaves) * head_step + k * part_step,   k < parts[h / kWaves]
-// and column `col` of it.  The item that begins a job writes it for the job's tokens.
+// and column `col` from its first on (up to 32, in two units).  The item that begins a job writes it for the job's tokens.
 struct Parts {
   int32_t first[kSets], parts[kSets];
 };
@@ -564,11 +565,19 @@ __device__ __forceinline__ int32_t chunks_of(const Job& x, float aim) {
 }
 __device__ __forceinline__ int32_t items_of(const Job& x) { return (x.cols + kWide - 1) / kWide * kHeads; }
 
+// 32-column blocks of an item of so many columns.
+__device__ __forceinline__ int32_t blocks_of(int32_t cols) { return cols <= kCols ? 1 : (cols <= 2 * kCols ? 2 : kWaves); }
+// Units of the parts of one chunk of an item job: two for each 32-column block and head.
+__device__ __forceinline__ int32_t units_of(const Job& x) {
+  const int32_t whole = (x.cols - 1) / kWide;             // column blocks before the last
+  return kHeads * kBlockUnits * (whole * kWaves + blocks_of(x.cols - whole * kWide));
+}
+
 struct Plan {
   int32_t j0, j1;                 // this thread's jobs
   Job first;                      // the first of them (mostly the only one)
   uint32_t tiles, streams;        // of streamed jobs before them
-  uint32_t items, units;          // items, and those that are parts, before them
+  uint32_t items, units;          // items, and units of those that are parts, before them
   uint32_t all_tiles, all_items, share, shares;    // tiles of a share, shares
   float aim;
 };
@@ -624,7 +633,7 @@ __device__ __forceinline__ Plan make_plan(const AttendArgs& a, const Lengths& n,
       const int32_t nch = chunks_of(x, p.aim);
       const uint32_t k = nch * items_of(x);
       items += k;
-      if (x.shared || x.split || nch > 1) units += k;
+      if (x.shared || x.split || nch > 1) units += nch * units_of(x);
     }
     p.items = items;
     p.units = units;
@@ -715,7 +724,7 @@ struct Item {
   Job x;
   int32_t valid, nch, tile0, tile1;     // chunks of the job's tiles, this item's tiles
   int32_t head, col0, blocks;           // first column, column blocks (1, 2 or 4)
-  int32_t unit, first;                  // its first part (-1: writes the output), first chunk and head
+  int32_t unit, width, first;           // its first unit (-1: writes the output), units; first chunk and head
   Parts parts;
 };
 
@@ -737,21 +746,27 @@ __device__ __forceinline__ void find_item(const AttendArgs& a, const Lengths& n,
       it.nch = nch;
       it.head = i % kHeads;
       it.col0 = (ncb - 1 - xb) * kWide;
-      it.blocks = x.cols - it.col0 <= kCols ? 1 : (x.cols - it.col0 <= 2 * kCols ? 2 : 4);
+      it.blocks = blocks_of(x.cols - it.col0);
       it.tile0 = min(t, chunk * len);
       it.tile1 = min(t, it.tile0 + len);
       it.first = chunk == 0 && it.head == 0;
-      it.unit = parts ? (int32_t)(a.stream_units + kWaves * (u + i)) : -1;
+      // units lie as the items do: by column block from the last (the only one that may be narrower), chunk and head
+      const int32_t width = kBlockUnits * it.blocks, narrow = kBlockUnits * blocks_of(x.cols - (ncb - 1) * kWide);
+      const int64_t begin = a.stream_units + (int64_t)u +
+                            (xb ? nch * kHeads * (narrow + (xb - 1) * (int64_t)(kBlockUnits * kWaves)) : 0);
+      const int64_t unit = begin + (chunk * kHeads + it.head) * width;
+      it.width = width;
+      it.unit = parts ? (int32_t)unit : -1;
       for (int v = 0; v < kSets; ++v) {
-        it.parts.first[v] = parts ? (int32_t)(a.stream_units + kWaves * (u + xb * nch * kHeads + v * kWaves)) : -1;
+        it.parts.first[v] = parts ? (int32_t)begin + v * kWaves * width : -1;
         it.parts.parts[v] = nch;
       }
       // only offsets that are not ascending make more parts than there is room for
-      it.valid = !parts || a.stream_units + (int64_t)kWaves * (u + i + 1) <= a.max_units;
+      it.valid = !parts || unit + width <= a.max_units;
       break;
     }
     at += k;
-    if (parts) u += k;
+    if (parts) u += nch * units_of(x);
   }
   __syncthreads();
 }
@@ -1086,7 +1101,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
     if (y.live) qf[d] = *reinterpret_cast<const u32x4*>(a.q + y.row * kDim + 16 * d + 8 * h);
   }
   if (it.first && turn == 0 && y.live && h == 0 && (c & (a.G - 1)) == 0)
-    describe(a, x, y, layer, it.parts, it.unit < 0 ? 0 : cb, kWaves, kWaves * kHeads, c);
+    describe(a, x, y, layer, it.parts, it.unit < 0 ? 0 : kBlockUnits * cb, it.width, it.width * kHeads, c);
   if (lane == 0) z.most[wave] = most;
   __syncthreads();                                   // the lengths' memory becomes the tiles'
 
@@ -1289,7 +1304,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
           st.o[d][r] = st.o[d][r] * f + g * o[4 * (c + kCols * (8 * d + 2 * (r >> 2) + h)) + (r & 3)];
     }
   }
-  write_state<BF16_OUT>(a, st, l, y, layer, unit < 0 ? -1 : unit + cb, lane);
+  write_state<BF16_OUT>(a, st, l, y, layer, unit < 0 ? -1 : unit + kBlockUnits * cb, lane);
 }
 
 template <bool BF16_OUT>
@@ -1372,10 +1387,10 @@ attend_join_kernel(const AttendArgs a, int32_t per) {
       at[which] = step[which] = 0;
       if (which == 1 && d[1].w == 0) continue;
       const int32_t first = set ? d0.z : d0.x, parts = set ? d0.w : d0.y, col = d1.z + hh;
-      const int32_t unit = first + (head % kWaves) * d1.x;
+      const int64_t unit = first + (int64_t)(head % kWaves) * d1.x, end = unit + (int64_t)(parts - 1) * d1.y;
       // holds for every token of a sequence; offsets that are not ascending may leave a token without parts
-      ok &= first >= 0 && parts >= 1 && parts <= a.max_units && d1.x >= 0 && d1.x <= kWaves && d1.y >= 0 && col >= 0 &&
-            col < a.unit_cols && unit + (int64_t)(parts - 1) * d1.y < a.max_units;
+      ok &= first >= 0 && parts >= 1 && parts <= a.max_units && d1.x >= 0 && d1.x <= kBlockUnits * kWaves && d1.y >= 0 &&
+            col >= 0 && col < kCols && end < a.max_units && end * a.unit_cols + col < (int64_t)a.max_units * a.unit_cols;
       n[which] = parts;
       at[which] = (layer * a.max_units + unit) * a.unit_cols + col;
       step[which] = (int64_t)d1.y * a.unit_cols;
@@ -1430,9 +1445,10 @@ attend_join_kernel(const AttendArgs a, int32_t per) {
 // Bounds for one layer.  Shares: the workgroups aimed at, one more next to items.  Streamed pieces: one for each
 // share and one more for each stream.  An item job of n > 16 columns has 8 ceil(n / 128) items a chunk, at most n / 2
 // (8 at 17, 16 at 129) and 8 + n / 16; the items of jobs cut into more chunks and the shares are together
-// at most the workgroups aimed at, and one.  Parts come from items of jobs that are cut, and in groups from all items of
-// the shared rows and of the own rows next to them: of sequences of up to kAlone columns, two or more in a run of a
-// group that shares.
+// at most the workgroups aimed at, and one.  Parts come from items of jobs that are cut (8 units of 16 columns at most),
+// and in groups from all items of the shared rows and of the own rows next to them: of sequences of up to kAlone
+// columns, two or more in a run of a group that shares.  Their columns are rounded up to 32, 64 or 128 at a job's
+// end, to less than twice as many and 63 more at most: in 8 heads up to n units and up to n / 2 + 32.
 struct Sizes {
   int32_t wgs, both_wgs, grid, unit_cols, stream_units, max_units;
   size_t desc, ml, acc, plans, total;
@@ -1448,11 +1464,11 @@ Sizes sizes_of(int64_t L, int64_t B, int64_t n_groups, int64_t n_q, int64_t G, b
   const int64_t jobs = least(B, n_q) + (grouped ? least(n_groups + cols / kAlone, least(B / 2, n_q)) : 0);
   const int64_t aimed = cols > kStreamCols ? z.both_wgs + 1 : z.wgs;
   const int64_t whole = cols > kStreamCols ? least(all_cols / 2, kHeads * jobs + all_cols / 16) : 0;
-  const int64_t parts = cols > kStreamCols ? aimed + least(shared_cols, kHeads * jobs + shared_cols / 8) : 0;
+  const int64_t parts = cols > kStreamCols ? kBlockUnits * kWaves * aimed + least(2 * shared_cols, 32 * jobs + shared_cols) : 0;
   z.grid = (int32_t)(aimed + whole);
-  z.unit_cols = (int32_t)least(cols, kCols);
+  z.unit_cols = (int32_t)least(cols, kStreamCols);
   z.stream_units = (int32_t)(kWaves * (aimed + kSets * jobs));
-  z.max_units = (int32_t)(z.stream_units + kWaves * parts);
+  z.max_units = (int32_t)(z.stream_units + parts);
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   z.desc = up((size_t)L * n_q * 4 * sizeof(int4));
   z.ml = up((size_t)L * z.max_units * z.unit_cols * sizeof(float2));

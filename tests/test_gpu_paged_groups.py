@@ -89,3 +89,16 @@ def test_each_sequence_its_own_group(dtype):
     x, y = attend(b, d, dtype, None), attend(b, d, dtype, b.i32(b.grp_off))
     check(b, d, x)
     assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("columns", [17, 32, 33, 64, 65, 96, 128, 129, 161, 193, 257])
+def test_columns_of_a_shared_job(columns, dtype):
+    """So many one-token sequences of one head per KV head, sharing rows that are cut into chunks: the parts of 32,
+    64 and 128 columns side by side, in a workspace of just its size."""
+    print("case: shared columns", columns, dtype, flush=True)
+    other = [3, 1, 40]
+    b = Batch([1] * columns + other, [300 + s % 7 for s in range(columns)] + [90, 30, 70], groups=[columns, 3],
+              ctx=[[900, 33]], pre=[256, 0], page=64, hq=8, seed=540 + columns, q_std=2.0)
+    d = b.to_device()
+    check(b, d, attend(b, d, dtype, d["grp_off"]))
