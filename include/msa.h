@@ -344,10 +344,11 @@ int msa_sparse_prefill(int32_t n_layers, int32_t B, int32_t T, int32_t Hq, const
  *                     of two up to MSA_MAX_PAGE_TOKENS
  *   page_table        [B][max_pages] int32: local row r of sequence b is row
  *                     r % page_tokens of page page_table[b][r / page_tokens], in every layer
- *   q_off             [B + 1] int32, ascending: the new tokens of sequence b are the packed
- *                     rows q_off[b] .. q_off[b + 1]) of k_new, v_new, q and the outputs (a
- *                     sequence may have none); packed rows from q_off[B] on are padding:
- *                     never used, and their output rows are left as they were
+ *   q_off             [B + 1] int32, ascending within [0, n_q]: the new tokens of sequence b are
+ *                     the packed rows q_off[b] .. q_off[b + 1]) of k_new, v_new, q and the
+ *                     outputs (a sequence may have none); packed rows before q_off[0] (those of
+ *                     other sequences) and from q_off[B] on (padding) are never used, and their
+ *                     output rows are left as they were
  *   kv_len            [B] int32: local rows of sequence b, its new tokens INCLUDED (they are
  *                     the last ones): new token i of n has local row kv_len[b] - n + i
  *

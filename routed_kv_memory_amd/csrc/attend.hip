@@ -1367,9 +1367,10 @@ attend_join_kernel(const AttendArgs a, int32_t per) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) d[i] = descs[(int64_t)t0 * 4 + i];
   const int32_t first_unit = descs[(int64_t)min(t0 + lane, a.n_q - 1) * 4].x;
-  const int32_t tn = min(t0 + per, clampi(a.q_off[a.B], 0, a.n_q));
+  // the sequences' tokens: those before and behind have no descriptor, or what an earlier call left there
+  const int32_t tb = clampi(a.q_off[0], 0, a.n_q), tn = min(t0 + per, clampi(a.q_off[a.B], 0, a.n_q));
   // per <= 64; a token whose first set has parts has parts of every set
-  uint64_t todo = __ballot(t0 + lane < tn && first_unit >= 0);
+  uint64_t todo = __ballot(t0 + lane >= tb && t0 + lane < tn && first_unit >= 0);
   for (; todo; todo &= todo - 1) {
     const int32_t t = t0 + __builtin_ctzll(todo);
     if (t != t0) {
