@@ -51,16 +51,18 @@ def tiles(rows):
     return max(1, -(-rows // 32))
 
 
-def batch(rows, layers, hq, seed, dtype, groups=None, lens=None):
-    """One new token a sequence; the sequences' pages are any of a small pool's."""
+def batch(rows, layers, hq, seed, dtype, groups=None, lens=None, new=None):
+    """One new token a sequence, or `new`; the sequences' pages are any of a small pool's."""
     B, most = len(rows), max(rows)
     gen = torch.Generator(device="cuda").manual_seed(seed)
     normal = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(BF16)
     i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
-    pool = 61
-    d = dict(q=normal(layers, B, hq, 128) * 2, q_off=list(range(B + 1)), kv_len=rows,
-             table=torch.randint(0, pool, (B, -(-most // PAGE)), generator=gen, device="cuda", dtype=torch.int32),
-             k_pages=normal(layers, pool, PAGE, 8, 128), v_pages=normal(layers, pool, PAGE, 8, 128))
+    pool, q_off = 61, [0]
+    for n in new or [1] * B:
+        q_off.append(q_off[-1] + n)
+    n_q = q_off[-1]
+    q, k_pages, v_pages = normal(layers, n_q, hq, 128) * 2, *(normal(layers, pool, PAGE, 8, 128) for _ in range(2))
+    table = torch.randint(0, pool, (B, -(-most // PAGE)), generator=gen, device="cuda", dtype=torch.int32)
     ctx, extra, n_groups = None, {}, B
     if groups:
         n_groups = len(groups)
@@ -71,12 +73,11 @@ def batch(rows, layers, hq, seed, dtype, groups=None, lens=None):
         ctx = (normal(layers, n_groups, most_ctx, 8, 128), normal(layers, n_groups, most_ctx, 8, 128), lens,
                [g for g, n in enumerate(groups) for _ in range(n)])
         extra = dict(grp_off=i32(off), ctx_k=ctx[0], ctx_v=ctx[1], ctx_len=i32(lens))
-    out = torch.full((layers, B, hq, 128), 7.0, dtype=dtype, device="cuda")
-    ws = torch.empty(msa.msa_paged_attend_workspace_size(layers, B, n_groups, B, hq), dtype=torch.uint8, device="cuda")
-    msa.msa_paged_attend(d["q"], i32(d["q_off"]), i32(rows), d["table"], d["k_pages"], d["v_pages"], SCALE, out,
-                         ws.fill_(0xFF), **extra)
+    out = torch.full((layers, n_q, hq, 128), 7.0, dtype=dtype, device="cuda")
+    ws = torch.empty(msa.msa_paged_attend_workspace_size(layers, B, n_groups, n_q, hq), dtype=torch.uint8, device="cuda")
+    msa.msa_paged_attend(q, i32(q_off), i32(rows), table, k_pages, v_pages, SCALE, out, ws.fill_(0xFF), **extra)
     torch.cuda.synchronize()
-    check_every_token(out, d["q"], d["q_off"], rows, d["table"], d["k_pages"], d["v_pages"], ctx)
+    check_every_token(out, q, q_off, rows, table, k_pages, v_pages, ctx)
 
 
 @pytest.mark.parametrize("sequences,pieces,cut", [
@@ -109,3 +110,19 @@ def test_groups():
     lists = [shares([tiles(r) for r in rows + c], 24) for c in lens]
     assert sum(any(n % 32 == 0 and cut for n, cut in x) for x in lists) >= 2
     batch(rows, 24, 8, 2, F32, groups=[7] * 40, lens=lens)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("layers,sequences,grouped", [(18, 330, False), (18, 330, True), (36, 203, True), (8, 700, False)])
+def test_streams_next_to_items(layers, sequences, grouped, dtype):
+    """One token each, and one sequence in fifty brings more: shares of many pieces beside shared tiles."""
+    print("case: streams next to items", layers, sequences, grouped, dtype, flush=True)
+    rng = random.Random(sequences + layers)
+    new = [rng.choice([17, 60, 140]) if s % 50 == 20 else 1 for s in range(sequences)]
+    rows = [n + rng.randint(0, 130) for n in new]
+    groups = [rng.randint(1, 9) for _ in range(sequences)] if grouped else None
+    if grouped:
+        groups = groups[:next(i for i in range(sequences) if sum(groups[:i]) >= sequences - 9)]
+        groups.append(sequences - sum(groups))
+    lens = [[rng.randint(0, 70) for _ in groups] for _ in range(layers)] if grouped else None
+    batch(rows, layers, 32, sequences, dtype, groups=groups, lens=lens, new=new)
