@@ -109,6 +109,7 @@ struct Lengths {
   // bit b: sequence b shares rows with none before it (first of its group, alone, or behind one that is)
   uint32_t* start;                // [kMaxSeqs / 32 + 1]
   uint32_t* sums;                 // [8][kWaves]
+  bool grouped;                   // whether any sequence may share: not where each is its own group
 };
 constexpr int kStartWords = kMaxSeqs / 32 + 1;
 constexpr int kStage = 1024;              // 16-byte words of a stage of shared tiles (below)
@@ -122,6 +123,7 @@ __device__ __forceinline__ Lengths lengths_in(u32x4* a, u32x4* b, u32x4* c, u32x
   n.grp = reinterpret_cast<int32_t*>(d);
   n.start = reinterpret_cast<uint32_t*>(n.off + kMaxSeqs + 4);
   n.sums = n.start + kStartWords + 3;
+  n.grouped = false;
   return n;
 }
 
@@ -138,15 +140,20 @@ __device__ __forceinline__ int32_t count_upto(const int32_t* a, int32_t n, int32
   return lo;
 }
 
-__device__ __forceinline__ void load_lengths(const AttendArgs& a, const Lengths& n, int64_t layer, int tid) {
+__device__ __forceinline__ void load_lengths(const AttendArgs& a, Lengths& n, int64_t layer, int tid) {
   const bool grouped = a.grp_off != nullptr;
+  bool own = a.n_groups == a.B;             // groups 0, 1, ... of one sequence each need no shared jobs
   const int32_t cap = a.max_pages << a.page_shift;
   for (int32_t i = tid; i <= a.B; i += kThreads) {
     n.off[i] = clampi(a.q_off[i], 0, a.n_q);
     if (i < a.B) n.len[i] = a.kv_len[i];
   }
   for (int32_t g = tid; g <= a.n_groups; g += kThreads) {
-    if (grouped) n.grp[g] = clampi(a.grp_off[g], 0, a.B);
+    if (grouped) {
+      const int32_t at = clampi(a.grp_off[g], 0, a.B);
+      n.grp[g] = at;
+      own &= at == g;
+    }
     if (g < a.n_groups) {
       n.clen[g] = a.max_ctx > 0 ? clampi(a.ctx_len[layer * a.n_groups + g], 0, a.max_ctx) : 0;
       n.pre[g] = grouped && a.pre_len ? clampi(a.pre_len[g], 0, cap) : 0;
@@ -154,8 +161,8 @@ __device__ __forceinline__ void load_lengths(const AttendArgs& a, const Lengths&
   }
   if (grouped)
     for (int i = tid; i < kStartWords; i += kThreads) n.start[i] = 0;
-  __syncthreads();
-  if (!grouped) return;
+  n.grouped = !__syncthreads_and(own) && grouped;
+  if (!n.grouped) return;
   auto mark = [&](int32_t b) { atomicOr(n.start + (b >> 5), 1u << (b & 31)); };
   for (int32_t g = tid; g <= a.n_groups; g += kThreads) mark(n.grp[g]);
   for (int32_t b = tid; b < a.B; b += kThreads)
@@ -178,7 +185,7 @@ __device__ __forceinline__ int32_t group_of(const AttendArgs& a, const Lengths& 
 // Job b < B: sequence b's rows.  Job B + b, in groups: the rows that the sequences from b on share (b the
 // first of them).
 __device__ __forceinline__ Job job_of(const AttendArgs& a, const Lengths& n, int32_t j) {
-  const bool grouped = a.grp_off != nullptr;
+  const bool grouped = n.grouped;
   Job x;
   const int32_t b = j < a.B ? j : j - a.B, cap = a.max_pages << a.page_shift;
   x.shared = j >= a.B;
@@ -584,7 +591,7 @@ struct Plan {
 
 __device__ __forceinline__ Plan make_plan(const AttendArgs& a, const Lengths& n, int tid) {
   Plan p;
-  const int32_t nj = a.grp_off ? 2 * a.B : a.B, per = (nj + kThreads - 1) / kThreads;
+  const int32_t nj = n.grouped ? 2 * a.B : a.B, per = (nj + kThreads - 1) / kThreads;
   p.j0 = min(nj, tid * per);
   p.j1 = min(nj, p.j0 + per);
   p.first.cols = 0;
@@ -812,7 +819,7 @@ __device__ __forceinline__ void attend_rows(uint16_t* tile, const u32x4* pv, con
 
 // A share of the streams; `tile` is the wave's.
 template <bool BF16_OUT>
-__device__ __forceinline__ void attend_streams(const AttendArgs& a, const Lengths& n, Plan p, Segment* seg, uint32_t* n_seg,
+__device__ __forceinline__ void attend_streams(const AttendArgs& a, Lengths& n, Plan p, Segment* seg, uint32_t* n_seg,
                                                uint16_t* tile, uint32_t number, int64_t layer, int tid) {
   constexpr int PARTS = BF16_OUT ? 1 : 3;
   static_assert(kStage * 16 >= kStreamRows * kVStride * 2, "a stage holds a wave's tile");
@@ -1323,7 +1330,7 @@ attend_kernel(const AttendArgs a) {
   const int64_t layer = blockIdx.x;
   const uint32_t id = blockIdx.z * gridDim.y + blockIdx.y;
   if (a.plans && id >= a.plans[layer * kThreads].shares + a.plans[layer * kThreads].all_items) return;
-  const Lengths n = lengths_in(stage0, stage1, stage2, stage3);
+  Lengths n = lengths_in(stage0, stage1, stage2, stage3);
   load_lengths(a, n, layer, tid);
   const Plan p = plan_of(a, n, layer, tid);
   // items that fit the chip at once are the longer ones (16 samples of one question: 173 us, shares first 179);
@@ -1345,7 +1352,7 @@ attend_kernel(const AttendArgs a) {
 __global__ void __launch_bounds__(kThreads)
 attend_plan_kernel(const AttendArgs a) {
   __shared__ u32x4 s0[kStage], s1[kStage], s2[kStage], s3[kStage];
-  const Lengths n = lengths_in(s0, s1, s2, s3);
+  Lengths n = lengths_in(s0, s1, s2, s3);
   load_lengths(a, n, blockIdx.x, threadIdx.x);
   a.plans[blockIdx.x * (int64_t)kThreads + threadIdx.x] = make_plan(a, n, threadIdx.x);
 }
