@@ -390,9 +390,10 @@ int msa_paged_append(int32_t n_layers, int32_t B, int32_t n_q, int32_t Hq, const
  * and b's local rows 0 .. kv_len[b] - n + i (causal, as msa_sparse_prefill).  The memory rows,
  * and the first pre_len[g] local rows where that is given, are read once for all sequences of
  * the group (those with so many new tokens that this saves nothing read them themselves): these
- * local rows must lie in the same pages in all of them (the first sequence's table is read).
- * pre_len changes only what is read, not what a token sees.  One new token a sequence is the decode, many are the prefill; both may be
- * mixed in one call.
+ * local rows must lie in the same pages in all of them.  Their pages are read from the table of the
+ * group's first sequence, also when that has no new tokens or fewer rows.  pre_len changes only what
+ * is read, not what a token sees.  One new token a sequence is the decode, many are the prefill; both
+ * may be mixed in one call.
  *
  *   q             [n_layers][n_q][Hq][128] bf16, Hq in {8, 16, 32, 64}
  *   grp_off       [n_groups + 1] int32, ascending from 0 to B (a group may have no sequence).  NULL
@@ -407,10 +408,12 @@ int msa_paged_append(int32_t n_layers, int32_t B, int32_t n_q, int32_t Hq, const
  * Scores, softmax and sums in fp32.  With fp32 output the probabilities enter the P.V product as
  * three bf16 parts (the fp32 value but for 2^-25 of it), with bf16 output as one bf16 value (its
  * rounding is the size of the output's own).  Rows a token does not see never reach its
- * output, infinities and NaN in them included.  Lengths are clamped to [0, max_ctx] and
- * [0, max_pages * page_tokens], page numbers to [0, n_pages).  A workspace serves one call at a
- * time.  Errors: NULL pointers, sizes < 1, n_groups > B, Hq % 8 != 0, page_tokens no power of
- * two, scale (SHAPE), the limits above (UNSUPPORTED), small workspace. */
+ * output, infinities and NaN in them included; sums of weights times V past fp32's range are
+ * infinite.  Lengths are clamped to [0, max_ctx] and [0, max_pages * page_tokens], page numbers to
+ * [0, n_pages); which row a token ends at follows from kv_len as it is given.  A workspace serves one
+ * call at a time.  Errors: NULL pointers (grp_off: unless n_groups == B), sizes < 1, n_groups > B,
+ * Hq % 8 != 0, page_tokens no power of two, scale (SHAPE), the limits above (UNSUPPORTED), small
+ * workspace. */
 size_t msa_paged_attend_workspace_size(int32_t n_layers, int32_t B, int32_t n_groups, int32_t n_q, int32_t Hq);
 int msa_paged_attend(int32_t n_layers, int32_t B, int32_t n_groups, int32_t n_q, int32_t Hq, const uint16_t* q,
                      const int32_t* q_off, const int32_t* grp_off, const uint16_t* ctx_k, const uint16_t* ctx_v,

@@ -6,7 +6,8 @@
 // k and v go to row r % P of page page_table[b][r / P], q to its own output.
 //
 // Bound: HBM (each byte is read once and written once, ~6 flop an element): 3.85 GB, 8,704 tokens of 32 query heads in
-// 18 layers, take 0.70-0.73 ms (5.3-5.5 TB/s), one token 6 us, where latency is all.  One wave takes one
+// 18 layers, take 0.70-0.73 ms (5.3-5.5 TB/s), one token 6 us, where latency is all (a launch and three loads that
+// wait for each other: q_off, the sequence's lengths, its page).  One wave takes one
 // token in one layer: 8 lanes a head hold the 8-dim pieces 8 j .. 8 j + 7 and 64 + 8 j .. + 7, so
 // both halves of every rotated pair sit in one lane, a row of 8 heads is one 2 KiB access of the
 // wave, and the token's 64 angles are formed once for all its heads (8 in each lane).  Angles are

@@ -22,8 +22,8 @@
 // attend_join_kernel joins where a column's rows were cut into parts; what is whole in one part has been
 // written by the workgroup that computed it.  (A workgroup that joins for the others would need a counter and
 // a device-wide release in each; the launch costs ~5 us.)
-// Measured: one token of 32 heads over 4,364 rows in 18 layers 61 us (4.9 TB/s); a prompt of 8,000 tokens over 4,300
-// memory rows 1.03-1.10 ms (980-1,044 TFLOP/s, bf16 output).  There the matrix cores are 50% busy and the
+// Measured: one token of 32 heads over 4,364 rows in 18 layers 61-73 us (4.1-4.9 TB/s); a prompt of 8,000 tokens over
+// 4,300 memory rows 1.03-1.12 ms (960-1,044 TFLOP/s, bf16 output).  There the matrix cores are 50% busy and the
 // vector units 44%; they overlap little, every instruction between a tile's barrier and its last product
 // shows in the time, and the clock gives way as the work gets denser (2.16 GHz at 1.18 ms, 1.94 at 1.07).
 // In both, S^T = K . Q^T is computed with K as the A operand and the columns as the B operand
@@ -50,7 +50,8 @@ constexpr int kStreamCols = 16;
 constexpr int kCols = 32;                 // columns of a wave that shares tiles
 // A sequence of more columns than this does not share its group's rows: parts of so many columns cost
 // more to write and join than the rows cost to read again (three sequences of 509 tokens, 32 heads, among 27 of
-// one token over 1,500 shared rows: 195 us, 256 us sharing; from 128 to 512 it is the same).
+// one token over 1,500 shared rows: 195 us, 256 us sharing; from 128 to 512 it is the same).  Eight sequences over 4,000
+// shared rows, two layers: 600 columns each 375 us, 459 sharing; 400 columns 278 us alone, 324 sharing as here.
 constexpr int kAlone = 512;
 constexpr int kWide = kWaves * kCols;     // columns of a workgroup of the second kind
 constexpr int kBlockUnits = kCols / kStreamCols;    // units of the workspace that its waves' columns take
@@ -66,7 +67,8 @@ constexpr int kSegments = 32;             // pieces of streams a workgroup lists
 // Two workgroups fit a CU (registers, LDS): 512 fill the chip.  A layer gets its share of them, but at
 // least kBothWgs where there are jobs of both kinds: items come in eights (the heads), and a handful of
 // eights would not split the work evenly.  16 samples of one question, 18 layers: 199 us with 28, 175 with 40,
-// 173 with 56, 186 with 64, 182 with 72.
+// 173 with 56, 186 with 64, 182 with 72.  Others are within 6% from 28 to 80: 36 layers 298-332 us (least with 28, 314
+// with 56), four questions in 12 layers 199-224 (least with 80, 210 with 56), a mixed batch in 18 layers 731-774.
 constexpr int kWgs = 512;
 constexpr int kBothWgs = 56;
 // A call of more workgroups than this has its plans made once, in a launch before: 2,048 sequences of 16 rows behind
@@ -419,7 +421,9 @@ __device__ __forceinline__ float below(float s, float scale2, float neg_m) {
 // value but for 2^-25 of it.  Two leave 2^-17: 2.3e-6 of the output against 4.3e-7 with three, for 850
 // against 985 us where the matrix cores bind (8 prompts of up to 1,088 tokens, 4 layers), next to nothing elsewhere.
 // PARTS 1 (bf16 output): one bf16 value, whose rounding (2^-8 of each weight) is the size of the
-// output's own; the sum is then taken of the rounded values, so the weights still add up to one.
+// output's own; the sum is then taken of the rounded values, so the weights still add up to one.  The output is then
+// off by 2.2e-3 (rms, relative; 1.7e-3 is the output's rounding alone).  Two parts take 1.46 ms where one takes 1.08 (the
+// long prompt), 236 against 186 us in a mixed batch, and in streams 183 against 175 us (64 users).
 template <int PARTS, bool CAREFUL>
 __device__ __forceinline__ void weights(const float* s, float scale2, float neg_m, u32x4* pw, float& l) {
 #pragma unroll
