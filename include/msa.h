@@ -422,6 +422,51 @@ int msa_paged_attend(int32_t n_layers, int32_t B, int32_t n_groups, int32_t n_q,
                      const int32_t* kv_len, const int32_t* pre_len, float scale, int32_t out_bf16, void* out,
                      void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------- paged local cache held in 4 bits
+ *
+ * [P5 推理全流程: the local KV grows token by token, and every step reads it]  The same cache with each
+ * row in 544 bytes instead of 2,048: 3.76 times the rows in the same memory and in the same read time.
+ * The 128 dims of a head are four blocks of 32; a block x is held as a power of two 2^e, e the smallest whole
+ * number with max|x| <= 7 * 2^e (kept in [-125, 125]), in a byte e + 127, and 32 codes of 4 bits: a sign
+ * (the high bit) and the index of the nearest of {0, 0.5, 1, 1.5, 2, 3, 4, 6} to |x| / 2^e (halfway: the even
+ * index; past 6: 6).  A code stands for the exact bf16 value (-1)^sign * element * 2^e.  A block that holds an infinity
+ * or NaN has the byte 255 and stands for NaN.  Of normally distributed values the rms error is 0.112 of their own rms.
+ *
+ *   k_pages, v_pages  [n_layers][n_pages][page_tokens * MSA_ROW4_BYTES] uint8, 16-byte aligned.  A page is [8 heads]
+ *                     [page_tokens][64] bytes of codes, dim 2 i in the low half of byte i, then [8][page_tokens][4]
+ *                     bytes of scales; page_tokens a power of two up to MSA_MAX_PAGE_TOKENS.  Any bytes may be read
+ *                     (scale bytes that the append does not write: 2^(byte - 127))
+ *
+ * page_table, q_off, kv_len and the limits as for the cache in bf16. */
+#define MSA_ROW4_BYTES 544
+
+/* msa_paged_append into a cache in 4 bits.  K is quantised from its value after norm and rotation before any rounding
+ * (computed in fp64 wherever fp32 leaves a code open: a row's bytes depend on its token alone), V from its bf16
+ * value; q is normed and turned in fp32 with one rounding to bf16, as msa_paged_append does.  theta == 0: no
+ * rotation (rows that are in position, of a cache in bf16 say; with w_k and w_q NULL they are
+ * quantised as they are).  Arguments, tokens that are not stored and errors else as msa_paged_append. */
+int msa_paged_append4(int32_t n_layers, int32_t B, int32_t n_q, int32_t Hq, const uint16_t* k_new,
+                      const uint16_t* v_new, const uint16_t* q, const int32_t* q_off, const int32_t* kv_len,
+                      const int32_t* pos_off, const int32_t* page_table, int32_t max_pages, int32_t page_tokens,
+                      int32_t n_pages, const uint16_t* w_k, const uint16_t* w_q, float eps, float theta,
+                      uint8_t* k_pages, uint8_t* v_pages, uint16_t* q_out, void* stream);
+
+/* Rows of a cache in 4 bits back in bf16, packed: what msa_pool_blocks takes to turn the rows of ended
+ * sequences into memory blocks, and msa_paged_append (or a copy) to move them elsewhere.  Packed row
+ * row_off[b] + i is local row row0[b] + i of sequence b, each code as the value it stands for; zeros where there
+ * is no such row (below 0, past the page table's row, on a page outside [0, n_pages)).
+ *
+ *   row_off       [B + 1] int32, ascending within [0, n_rows]; packed rows before row_off[0] and from row_off[B] on
+ *                 are left as they were
+ *   row0          [B] int32, or NULL for 0
+ *   k_out, v_out  [n_layers][n_rows][8][128] bf16
+ *
+ * n_rows <= MSA_MAX_NEW_TOKENS; n_rows == 0 enqueues nothing (k_out, v_out may be NULL).  Errors: NULL pointers,
+ * sizes < 1, page_tokens no power of two, unaligned arrays (SHAPE), the limits (UNSUPPORTED). */
+int msa_paged_read4(int32_t n_layers, int32_t B, int32_t n_rows, const int32_t* row_off, const int32_t* row0,
+                    const int32_t* page_table, int32_t max_pages, int32_t page_tokens, int32_t n_pages,
+                    const uint8_t* k_pages, const uint8_t* v_pages, uint16_t* k_out, uint16_t* v_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

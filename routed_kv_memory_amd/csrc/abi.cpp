@@ -529,3 +529,44 @@ MSA_API int msa_paged_attend(int32_t n_layers, int32_t B, int32_t n_groups, int3
                                        as_stream(stream)),
                     "msa_paged_attend");
 }
+
+// ------------------------------------------------- paged local cache held in 4 bits
+
+MSA_API int msa_paged_append4(int32_t n_layers, int32_t B, int32_t n_q, int32_t Hq, const uint16_t* k_new,
+                              const uint16_t* v_new, const uint16_t* q, const int32_t* q_off, const int32_t* kv_len,
+                              const int32_t* pos_off, const int32_t* page_table, int32_t max_pages,
+                              int32_t page_tokens, int32_t n_pages, const uint16_t* w_k, const uint16_t* w_q,
+                              float eps, float theta, uint8_t* k_pages, uint8_t* v_pages, uint16_t* q_out,
+                              void* stream) {
+  if (!q_off || !kv_len || !page_table || !k_pages || !v_pages || (n_q > 0 && (!k_new || !v_new)) || (q && !q_out))
+    return fail(MSA_ERR_NULL, "msa_paged_append4: null pointer");
+  if (!all_aligned16({k_new, v_new, q, w_k, w_q, k_pages, v_pages, q ? q_out : nullptr}))
+    return fail(MSA_ERR_SHAPE, "msa_paged_append4: bf16 arrays and pages must be 16-byte aligned");
+  int st = check_paged_sizes("msa_paged_append4", n_layers, B, n_q, max_pages, page_tokens, n_pages);
+  if (!st && q) st = check_heads("msa_paged_append4", Hq);
+  if (st) return st;
+  if (!(eps >= 0.f) || !(eps < __builtin_inff()) || !(theta >= 0.f) || !(theta < __builtin_inff()))
+    return fail(MSA_ERR_SHAPE, "msa_paged_append4: eps=%g theta=%g", (double)eps, (double)theta);
+  if (n_q == 0) return MSA_OK;
+  return hip_status(msa::launch_append4(n_layers, B, n_q, Hq, k_new, v_new, q, q_off, kv_len, pos_off, page_table,
+                                        max_pages, page_shift_of(page_tokens), n_pages, w_k, w_q, eps, theta, k_pages,
+                                        v_pages, q_out, as_stream(stream)),
+                    "msa_paged_append4");
+}
+
+MSA_API int msa_paged_read4(int32_t n_layers, int32_t B, int32_t n_rows, const int32_t* row_off, const int32_t* row0,
+                            const int32_t* page_table, int32_t max_pages, int32_t page_tokens, int32_t n_pages,
+                            const uint8_t* k_pages, const uint8_t* v_pages, uint16_t* k_out, uint16_t* v_out,
+                            void* stream) {
+  if (!row_off || !page_table || !k_pages || !v_pages || (n_rows > 0 && (!k_out || !v_out)))
+    return fail(MSA_ERR_NULL, "msa_paged_read4: null pointer");
+  if (!all_aligned16({k_pages, v_pages, k_out, v_out}))
+    return fail(MSA_ERR_SHAPE, "msa_paged_read4: pages and outputs must be 16-byte aligned");
+  const int st = check_paged_sizes("msa_paged_read4", n_layers, B, n_rows, max_pages, page_tokens, n_pages);
+  if (st) return st;
+  if (n_rows == 0) return MSA_OK;
+  return hip_status(msa::launch_read4(n_layers, B, n_rows, row_off, row0, page_table, max_pages,
+                                      page_shift_of(page_tokens), n_pages, k_pages, v_pages, k_out, v_out,
+                                      as_stream(stream)),
+                    "msa_paged_read4");
+}

@@ -14,73 +14,13 @@
 // formed and reduced to a fraction of a turn in fp64 (far positions lose their fraction in fp32):
 // theta^(-e/64) for e = 8 j + i is a product of four powers the host passes, 10 fp64 products.
 // Everything in between is fp32; one rounding to bf16.
-#include "msa_device.hpp"
+#include "append_core.hpp"
 #include "msa_kernels.hpp"
-
-#include <cmath>
 
 namespace msa {
 namespace {
 
 constexpr int kAppendWaves = 4;            // tokens per workgroup
-
-// theta^(-1/64), its 8th, 16th and 32nd power
-struct Turns {
-  double r1, r8, r16, r32;
-};
-
-__device__ __forceinline__ void unpack8(u32x4 w, float* f) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo(w[i]);
-    f[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
-
-__device__ __forceinline__ u32x4 pack8(const float* f) {
-  u32x4 w;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = pack2_bf16(f[2 * i], f[2 * i + 1]);
-  return w;
-}
-
-// Sum over the 8 lanes of a head (an aligned half of a DPP row); every lane gets it.
-__device__ __forceinline__ float lanes8_sum(float v) {
-  int x = __float_as_int(v);
-  v += __int_as_float(__builtin_amdgcn_update_dpp(x, x, 0xB1, 0xF, 0xF, false));    // quad_perm [1,0,3,2]
-  x = __float_as_int(v);
-  v += __int_as_float(__builtin_amdgcn_update_dpp(x, x, 0x4E, 0xF, 0xF, false));    // quad_perm [2,3,0,1]
-  x = __float_as_int(v);
-  return v + __int_as_float(__builtin_amdgcn_update_dpp(x, x, 0x141, 0xF, 0xF, false));   // row_half_mirror
-}
-
-// One head's row in 8 lanes: lo = dims 8 j .., hi = dims 64 + 8 j ..; normed (w != NULL) and turned.
-template <bool NORM>
-__device__ __forceinline__ void norm_turn(u32x4& lo, u32x4& hi, const float* w_lo, const float* w_hi, float eps,
-                                          const float* cs, const float* sn) {
-  float a[8], b[8];
-  unpack8(lo, a);
-  unpack8(hi, b);
-  if (NORM) {
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss += a[i] * a[i] + b[i] * b[i];
-    const float inv = 1.0f / sqrtf(lanes8_sum(ss) * (1.0f / kDim) + eps);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      a[i] *= inv * w_lo[i];
-      b[i] *= inv * w_hi[i];
-    }
-  }
-  float x[8], y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] = a[i] * cs[i] - b[i] * sn[i];
-    y[i] = b[i] * cs[i] + a[i] * sn[i];
-  }
-  lo = pack8(x);
-  hi = pack8(y);
-}
 
 template <bool NORM_K, bool NORM_Q>
 __global__ void __launch_bounds__(64 * kAppendWaves)
@@ -108,13 +48,7 @@ append_kernel(int32_t B, int32_t n_q, int32_t Hq, const uint16_t* __restrict__ k
               v_hi = *reinterpret_cast<const u32x4*>(v_new + at + 64);
 
   float cs[8], sn[8];
-  double f = (j & 1 ? pw.r8 : 1.0) * (j & 2 ? pw.r16 : 1.0) * (j & 4 ? pw.r32 : 1.0) * 0.15915494309189533577;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const double turns = pos * f;
-    sincospif((float)(2.0 * (turns - rint(turns))), &sn[i], &cs[i]);
-    f *= pw.r1;
-  }
+  angles(pos, j, pw, cs, sn);
   float w_lo[8], w_hi[8];
   if (NORM_K) {
     unpack8(*reinterpret_cast<const u32x4*>(w_k + layer * kDim + 8 * j), w_lo);
@@ -156,8 +90,7 @@ hipError_t launch_append(int32_t L, int32_t B, int32_t n_q, int32_t Hq, const ui
                          const int32_t* page_table, int32_t max_pages, int32_t page_shift, int32_t n_pages,
                          const uint16_t* w_k, const uint16_t* w_q, float eps, float theta, uint16_t* k_pages,
                          uint16_t* v_pages, uint16_t* q_out, hipStream_t s) {
-  const double l = std::log2((double)theta);
-  const Turns pw = {std::exp2(-l / 64), std::exp2(-l / 8), std::exp2(-l / 4), std::exp2(-l / 2)};
+  const Turns pw = turns_of(theta);
   const dim3 grid((unsigned)((n_q + kAppendWaves - 1) / kAppendWaves), (unsigned)L);
 #define MSA_APPEND_LAUNCH(NK, NQ)                                                                                  \
   hipLaunchKernelGGL((append_kernel<NK, NQ>), grid, dim3(64 * kAppendWaves), 0, s, B, n_q, Hq, k_new, v_new, q,   \

@@ -63,6 +63,17 @@ hipError_t launch_append(int32_t L, int32_t B, int32_t n_q, int32_t Hq, const ui
                          const uint16_t* w_k, const uint16_t* w_q, float eps, float theta, uint16_t* k_pages,
                          uint16_t* v_pages, uint16_t* q_out, hipStream_t s);
 
+// append4.hip, read4.hip
+hipError_t launch_append4(int32_t L, int32_t B, int32_t n_q, int32_t Hq, const uint16_t* k_new, const uint16_t* v_new,
+                          const uint16_t* q, const int32_t* q_off, const int32_t* kv_len, const int32_t* pos_off,
+                          const int32_t* page_table, int32_t max_pages, int32_t page_shift, int32_t n_pages,
+                          const uint16_t* w_k, const uint16_t* w_q, float eps, float theta, uint8_t* k_pages,
+                          uint8_t* v_pages, uint16_t* q_out, hipStream_t s);
+hipError_t launch_read4(int32_t L, int32_t B, int32_t n_rows, const int32_t* row_off, const int32_t* row0,
+                        const int32_t* page_table, int32_t max_pages, int32_t page_shift, int32_t n_pages,
+                        const uint8_t* k_pages, const uint8_t* v_pages, uint16_t* k_out, uint16_t* v_out,
+                        hipStream_t s);
+
 // attend.hip
 size_t attend_workspace_bytes(int32_t L, int32_t B, int32_t n_groups, int32_t n_q, int32_t Hq);
 hipError_t launch_attend(int32_t L, int32_t B, int32_t n_groups, int32_t n_q, int32_t Hq, const uint16_t* q,

@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_PKG, "libmsa_san.so" if os.environ.get("MSA_SANITIZED")
 
 MSA_OK, MSA_ERR_NULL, MSA_ERR_SHAPE, MSA_ERR_UNSUPPORTED, MSA_ERR_WORKSPACE, MSA_ERR_HIP = range(6)
 HEADS, HEAD_DIM, BLOCK_TOKENS, TILE_BLOCKS, MAX_TOPK = 8, 128, 64, 16, 256
+ROW4_BYTES = 544            # of a row of the paged local cache held in 4 bits
 
 
 class MsaError(RuntimeError):
@@ -58,6 +59,9 @@ _SIGS = {
     "msa_paged_attend_workspace_size": ([_I32, _I32, _I32, _I32, _I32], _SZ),
     "msa_paged_attend": ([_I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _P, _I32, _P,
                           _P, _F32, _I32, _P, _P, _SZ, _P], ctypes.c_int),
+    "msa_paged_append4": ([_I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _F32, _F32, _P,
+                           _P, _P, _P], ctypes.c_int),
+    "msa_paged_read4": ([_I32, _I32, _I32, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _P, _P], ctypes.c_int),
 }
 
 _lib = None
@@ -423,3 +427,60 @@ def msa_paged_attend(q, q_off, kv_len, page_table, k_pages, v_pages, scale, out,
         _on(dev, pre_len, _I32T, (n_groups,), "pre_len"), float(scale), 0 if out.dtype == torch.float32 else 1,
         _on(dev, out, _F32_BF16, heads, "out", o_shape), _on(dev, workspace, _ANY, None, "workspace"),
         workspace.numel() * workspace.element_size()))
+
+
+# ------------------------------------------------------------------ paged local cache held in 4 bits
+
+_U8 = (torch.uint8,)
+
+
+def _pages4(k_pages):
+    """Shape, pages and tokens a page of [L][n_pages][page_tokens * 544]."""
+    p_shape = _dims(k_pages, 3, "k_pages")
+    if p_shape[2] % ROW4_BYTES:
+        raise ValueError("k_pages has pages of %d bytes, expected a multiple of %d" % (p_shape[2], ROW4_BYTES))
+    return p_shape, p_shape[1], p_shape[2] // ROW4_BYTES
+
+
+def msa_paged_append4(k_new, v_new, q, q_off, kv_len, page_table, k_pages, v_pages, q_out, eps, theta, pos_off=None,
+                      w_k=None, w_q=None, stream=None):
+    """msa_paged_append into pages in 4 bits: k_pages, v_pages [L][n_pages][page_tokens * ROW4_BYTES] uint8;
+    theta 0 for no rotation; the other arguments as there."""
+    k_shape = _dims(k_new, 4, "k_new")
+    L, n_q = k_shape[0], k_shape[1]
+    p_shape, n_pages, page_tokens = _pages4(k_pages)
+    B, max_pages = _dims(page_table, 2, "page_table")
+    _required(v_new=v_new, q_off=q_off, kv_len=kv_len, v_pages=v_pages)
+    if q is None:
+        Hq, q_out, w_q, q_shape = 0, None, None, None
+    else:
+        q_shape = _dims(q, 4, "q")
+        Hq = q_shape[2]
+        _required(q_out=q_out)
+    dev = k_new.get_device()
+    new, pages, heads = (L, n_q, HEADS, HEAD_DIM), (L, n_pages, p_shape[2]), (L, n_q, Hq, HEAD_DIM)
+    _call("msa_paged_append4", dev, stream, (
+        L, B, n_q, Hq, _on(dev, k_new, _BF16, new, "k_new", k_shape), _on(dev, v_new, _BF16, new, "v_new"),
+        _on(dev, q, _BF16, heads, "q", q_shape), _on(dev, q_off, _I32T, (B + 1,), "q_off"),
+        _on(dev, kv_len, _I32T, (B,), "kv_len"), _on(dev, pos_off, _I32T, (B,), "pos_off"),
+        _on(dev, page_table, _I32T, None, "page_table"), max_pages, page_tokens, n_pages,
+        _on(dev, w_k, _BF16, (L, HEAD_DIM), "w_k"), _on(dev, w_q, _BF16, (L, HEAD_DIM), "w_q"), float(eps),
+        float(theta), _on(dev, k_pages, _U8, pages, "k_pages", p_shape), _on(dev, v_pages, _U8, pages, "v_pages"),
+        _on(dev, q_out, _BF16, heads, "q_out")))
+
+
+def msa_paged_read4(k_pages, v_pages, row_off, page_table, k_out, v_out, row0=None, stream=None):
+    """k_pages, v_pages as for msa_paged_append4; row_off [B+1], page_table [B][max_pages], row0 [B] int32 (None:
+    from row 0 on); k_out, v_out [L][n_rows][8][128] bf16."""
+    p_shape, n_pages, page_tokens = _pages4(k_pages)
+    B, max_pages = _dims(page_table, 2, "page_table")
+    o_shape = _dims(k_out, 4, "k_out")
+    _required(v_pages=v_pages, row_off=row_off, v_out=v_out)
+    L, n_rows = p_shape[0], o_shape[1]
+    dev = k_pages.get_device()
+    rows = (L, n_rows, HEADS, HEAD_DIM)
+    _call("msa_paged_read4", dev, stream, (
+        L, B, n_rows, _on(dev, row_off, _I32T, (B + 1,), "row_off"), _on(dev, row0, _I32T, (B,), "row0"),
+        _on(dev, page_table, _I32T, None, "page_table"), max_pages, page_tokens, n_pages,
+        _on(dev, k_pages, _U8, None, "k_pages"), _on(dev, v_pages, _U8, p_shape, "v_pages"),
+        _on(dev, k_out, _BF16, rows, "k_out", o_shape), _on(dev, v_out, _BF16, rows, "v_out")))
