@@ -467,6 +467,17 @@ int msa_paged_read4(int32_t n_layers, int32_t B, int32_t n_rows, const int32_t* 
                     const int32_t* page_table, int32_t max_pages, int32_t page_tokens, int32_t n_pages,
                     const uint8_t* k_pages, const uint8_t* v_pages, uint16_t* k_out, uint16_t* v_out, void* stream);
 
+/* msa_paged_attend over local rows in 4 bits, read as the values they stand for; the memory rows stay in bf16.
+ * Groups, shared rows, what a token sees, the output and its rounding, limits, workspace and errors as there; of a page,
+ * rows that a token does not see never reach its output, blocks that stand for NaN included. */
+size_t msa_paged_attend4_workspace_size(int32_t n_layers, int32_t B, int32_t n_groups, int32_t n_q, int32_t Hq);
+int msa_paged_attend4(int32_t n_layers, int32_t B, int32_t n_groups, int32_t n_q, int32_t Hq, const uint16_t* q,
+                      const int32_t* q_off, const int32_t* grp_off, const uint16_t* ctx_k, const uint16_t* ctx_v,
+                      const int32_t* ctx_len, int32_t max_ctx, const uint8_t* k_pages, const uint8_t* v_pages,
+                      int32_t n_pages, int32_t page_tokens, const int32_t* page_table, int32_t max_pages,
+                      const int32_t* kv_len, const int32_t* pre_len, float scale, int32_t out_bf16, void* out,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,7 +12,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmsa.so")
 LIB_SAN = os.path.join(PKG, "libmsa_san.so")
 SOURCES = ["abi.cpp", "pool.hip", "route.hip", "topk.hip", "gather.hip", "decode.hip", "prefill.hip", "encode.hip",
-           "append.hip", "attend.hip", "append4.hip", "read4.hip"]
+           "append.hip", "attend.hip", "append4.hip", "read4.hip",
+           "attend4.hip"]
 ARCH = os.environ.get("MSA_OFFLOAD_ARCH", "gfx950")
 FLAGS = ["-O3", "-fPIC", "-std=c++17", "-fvisibility=hidden", "--offload-arch=" + ARCH,
          # packed fp32 VALU forms are kept out of generated code

@@ -496,6 +496,37 @@ MSA_API size_t msa_paged_attend_workspace_size(int32_t n_layers, int32_t B, int3
   return msa::attend_workspace_bytes(n_layers, B, n_groups, n_q, Hq) + 256;
 }
 
+namespace {
+
+// what the attention checks whatever the pages are held in
+int check_attend(const char* fn, int32_t n_layers, int32_t B, int32_t n_groups, int32_t n_q, int32_t Hq, const void* q,
+                 const int32_t* q_off, const int32_t* grp_off, const void* ctx_k, const void* ctx_v, const int32_t* ctx_len,
+                 int32_t max_ctx, const void* k_pages, const void* v_pages, int32_t n_pages, int32_t page_tokens,
+                 const int32_t* page_table, int32_t max_pages, const int32_t* kv_len, float scale, int32_t out_bf16,
+                 const void* out, const void* workspace, size_t workspace_bytes) {
+  if (!q_off || !page_table || !kv_len || !k_pages || !v_pages || !workspace || (n_q > 0 && (!q || !out)))
+    return fail(MSA_ERR_NULL, "%s: null pointer", fn);
+  if (max_ctx > 0 && (!ctx_k || !ctx_v || !ctx_len)) return fail(MSA_ERR_NULL, "%s: null memory context", fn);
+  if (!all_aligned16({q, max_ctx > 0 ? ctx_k : nullptr, max_ctx > 0 ? ctx_v : nullptr, k_pages, v_pages, out}))
+    return fail(MSA_ERR_SHAPE, "%s: q, K/V and out must be 16-byte aligned", fn);
+  int st = check_paged_sizes(fn, n_layers, B, n_q, max_pages, page_tokens, n_pages);
+  if (!st) st = check_heads(fn, Hq);
+  if (st) return st;
+  if (n_groups < 1 || n_groups > B || max_ctx < 0)
+    return fail(MSA_ERR_SHAPE, "%s: n_groups=%d B=%d max_ctx=%d", fn, n_groups, B, max_ctx);
+  if (n_groups < B && !grp_off) return fail(MSA_ERR_NULL, "%s: null grp_off", fn);
+  if (max_ctx > MSA_MAX_LOCAL_ROWS) return fail(MSA_ERR_UNSUPPORTED, "%s: max_ctx=%d", fn, max_ctx);
+  if (!(scale > 0.f) || !(scale * 1.4426950408889634f < __builtin_inff()))     // the kernel's scores are in log2 units
+    return fail(MSA_ERR_SHAPE, "%s: scale=%g must be positive and below 2.3e38", fn, (double)scale);
+  if (out_bf16 != 0 && out_bf16 != 1) return fail(MSA_ERR_SHAPE, "%s: out_bf16=%d", fn, out_bf16);
+  const size_t need = msa_paged_attend_workspace_size(n_layers, B, n_groups, n_q, Hq);
+  if (workspace_bytes < need)
+    return fail(MSA_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
+  return MSA_OK;
+}
+
+}  // namespace
+
 MSA_API int msa_paged_attend(int32_t n_layers, int32_t B, int32_t n_groups, int32_t n_q, int32_t Hq, const uint16_t* q,
                              const int32_t* q_off, const int32_t* grp_off, const uint16_t* ctx_k,
                              const uint16_t* ctx_v, const int32_t* ctx_len, int32_t max_ctx, const uint16_t* k_pages,
@@ -503,24 +534,10 @@ MSA_API int msa_paged_attend(int32_t n_layers, int32_t B, int32_t n_groups, int3
                              const int32_t* page_table, int32_t max_pages, const int32_t* kv_len,
                              const int32_t* pre_len, float scale, int32_t out_bf16, void* out, void* workspace,
                              size_t workspace_bytes, void* stream) {
-  if (!q_off || !page_table || !kv_len || !k_pages || !v_pages || !workspace || (n_q > 0 && (!q || !out)))
-    return fail(MSA_ERR_NULL, "msa_paged_attend: null pointer");
-  if (max_ctx > 0 && (!ctx_k || !ctx_v || !ctx_len)) return fail(MSA_ERR_NULL, "msa_paged_attend: null memory context");
-  if (!all_aligned16({q, max_ctx > 0 ? ctx_k : nullptr, max_ctx > 0 ? ctx_v : nullptr, k_pages, v_pages, out}))
-    return fail(MSA_ERR_SHAPE, "msa_paged_attend: q, K/V and out must be 16-byte aligned");
-  int st = check_paged_sizes("msa_paged_attend", n_layers, B, n_q, max_pages, page_tokens, n_pages);
-  if (!st) st = check_heads("msa_paged_attend", Hq);
+  const int st = check_attend("msa_paged_attend", n_layers, B, n_groups, n_q, Hq, q, q_off, grp_off, ctx_k, ctx_v, ctx_len,
+                              max_ctx, k_pages, v_pages, n_pages, page_tokens, page_table, max_pages, kv_len, scale,
+                              out_bf16, out, workspace, workspace_bytes);
   if (st) return st;
-  if (n_groups < 1 || n_groups > B || max_ctx < 0)
-    return fail(MSA_ERR_SHAPE, "msa_paged_attend: n_groups=%d B=%d max_ctx=%d", n_groups, B, max_ctx);
-  if (n_groups < B && !grp_off) return fail(MSA_ERR_NULL, "msa_paged_attend: null grp_off");
-  if (max_ctx > MSA_MAX_LOCAL_ROWS) return fail(MSA_ERR_UNSUPPORTED, "msa_paged_attend: max_ctx=%d", max_ctx);
-  if (!(scale > 0.f) || !(scale * 1.4426950408889634f < __builtin_inff()))     // the kernel's scores are in log2 units
-    return fail(MSA_ERR_SHAPE, "msa_paged_attend: scale=%g must be positive and below 2.3e38", (double)scale);
-  if (out_bf16 != 0 && out_bf16 != 1) return fail(MSA_ERR_SHAPE, "msa_paged_attend: out_bf16=%d", out_bf16);
-  const size_t need = msa_paged_attend_workspace_size(n_layers, B, n_groups, n_q, Hq);
-  if (workspace_bytes < need)
-    return fail(MSA_ERR_WORKSPACE, "msa_paged_attend: workspace %zu < %zu bytes", workspace_bytes, need);
   if (n_q == 0) return MSA_OK;
   void* ws = reinterpret_cast<void*>(align256(reinterpret_cast<size_t>(workspace)));
   return hip_status(msa::launch_attend(n_layers, B, n_groups, n_q, Hq, q, q_off, grp_off, ctx_k, ctx_v, ctx_len,
@@ -569,4 +586,29 @@ MSA_API int msa_paged_read4(int32_t n_layers, int32_t B, int32_t n_rows, const i
                                       page_shift_of(page_tokens), n_pages, k_pages, v_pages, k_out, v_out,
                                       as_stream(stream)),
                     "msa_paged_read4");
+}
+
+MSA_API size_t msa_paged_attend4_workspace_size(int32_t n_layers, int32_t B, int32_t n_groups, int32_t n_q,
+                                                int32_t Hq) {
+  return msa_paged_attend_workspace_size(n_layers, B, n_groups, n_q, Hq);      // the same parts
+}
+
+MSA_API int msa_paged_attend4(int32_t n_layers, int32_t B, int32_t n_groups, int32_t n_q, int32_t Hq, const uint16_t* q,
+                             const int32_t* q_off, const int32_t* grp_off, const uint16_t* ctx_k,
+                             const uint16_t* ctx_v, const int32_t* ctx_len, int32_t max_ctx, const uint8_t* k_pages,
+                             const uint8_t* v_pages, int32_t n_pages, int32_t page_tokens,
+                             const int32_t* page_table, int32_t max_pages, const int32_t* kv_len,
+                             const int32_t* pre_len, float scale, int32_t out_bf16, void* out, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  const int st = check_attend("msa_paged_attend4", n_layers, B, n_groups, n_q, Hq, q, q_off, grp_off, ctx_k, ctx_v, ctx_len,
+                              max_ctx, k_pages, v_pages, n_pages, page_tokens, page_table, max_pages, kv_len, scale,
+                              out_bf16, out, workspace, workspace_bytes);
+  if (st) return st;
+  if (n_q == 0) return MSA_OK;
+  void* ws = reinterpret_cast<void*>(align256(reinterpret_cast<size_t>(workspace)));
+  return hip_status(msa::launch_attend4(n_layers, B, n_groups, n_q, Hq, q, q_off, grp_off, ctx_k, ctx_v, ctx_len,
+                                       max_ctx, k_pages, v_pages, n_pages, page_shift_of(page_tokens),
+                                       page_table, max_pages, kv_len, pre_len, scale, out_bf16 == 1, out, ws,
+                                       as_stream(stream)),
+                    "msa_paged_attend4");
 }

@@ -256,7 +256,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
   for (int i = 0; i < kPer; ++i) {
     const int r = 4 * i + (lane >> 4);
     k_lane[i] = 2 * (r * kRow + 8 * ((lane & 15) ^ ((w8 + r) & 15)));
-    v_lane[i] = 2 * (r * kRow + 8 * ((lane & 15) ^ (4 * (lane >> 4))));
+    v_lane[i] = 2 * (r * kRow + 8 * ((lane & 15) ^ (5 * (lane >> 4))));
   }
   // the page of the wave's rows of a page tile, as it stands in the table: a scalar load (a vector load's result
   // would only come after all the tile loads issued before it), not waited for before the tile's turn

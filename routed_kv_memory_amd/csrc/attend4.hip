@@ -1,0 +1,409 @@
+// attend4.hip -- attention of ragged new tokens over [memory context ; paged local rows held in 4 bits].
+//
+// What attend.hip computes, over local rows in the format of cache4.hpp; the memory rows are bf16.  A code stands
+// for an exact bf16 value, so the rows are turned into those on the way to the matrix cores, and the arithmetic is that
+// of the attention over rows in bf16.
+//
+// - Jobs of up to 16 columns: a wave streams rows.  A local tile of 128 rows has the bytes of a memory tile of 32.
+//   K codes are loaded as the first product's A operand takes them (lane l: 32 dims, a block with its scale, of row
+//   l & 15) and turned into bf16 in registers; V goes through the wave's LDS tile, 32 rows at a time.
+// - More columns: 4 waves share tiles of 32 rows, which are turned into bf16 on the way into LDS.
+#include "attend_core.hpp"
+#include "cache4.hpp"
+
+namespace msa {
+namespace {
+
+struct Rows4 {
+  static constexpr int kStreamLocal = 128;
+};
+
+// A share of the streams; `tile` is the wave's.
+template <bool BF16_OUT>
+__device__ __forceinline__ void attend_streams(const AttendArgs& a, Lengths& n, Plan p, Segment* seg, uint32_t* n_seg,
+                                               uint16_t* tile, uint32_t number, int64_t layer, int tid) {
+  constexpr int PARTS = BF16_OUT ? 1 : 3;
+  constexpr int kLocal = Rows4::kStreamLocal;
+  static_assert(kLocal == 128, "two rows a lane are found, four pieces of 32 used");
+  static_assert(kStage * 16 >= kStreamRows * kVStride * 2, "a stage holds a wave's tile");
+  const int lane = tid & 63, wave = tid >> 6;
+  const int j = lane & 15, g = lane >> 4;
+  auto uni = [](int32_t v) { return __builtin_amdgcn_readfirstlane(v); };
+
+  const uint16_t *ctx_k = kept(a.ctx_k), *ctx_v = kept(a.ctx_v);
+  const int32_t max_ctx = kept(a.max_ctx), shift = kept(a.page_shift);
+  const int64_t ctx_row = kept(layer * a.n_groups * (int64_t)a.max_ctx);
+  const int64_t layer_at = ((layer * a.n_pages) << shift) * kRow4;
+  const uint8_t *page_k = kept((const uint8_t*)a.k_pages + layer_at), *page_v = kept((const uint8_t*)a.v_pages + layer_at);
+
+  for (uint32_t from = 0;;) {
+    if (tid < 3) n_seg[tid] = 0;
+    __syncthreads();
+    const uint32_t reached = list_segments<Rows4>(a, n, p, seg, n_seg, number, from);
+    const int32_t ns = uni((int32_t)n_seg[0]);
+    __syncthreads();                              // the lengths' memory becomes the tiles'
+
+    // Three cursors across the pieces: `l` is used; `w` is loaded, piece by piece into the registers that l's rows
+    // leave; the rows of `x` are looked up (lane r the r-th and the 64 + r-th of the tile).
+    struct Cursor {
+      int32_t s, tile, tile1, nctx, c, p0, p1, seq, grp, head;
+    } l, w, x;
+    auto enter = [&](Cursor& u, int32_t s) __attribute__((always_inline)) {
+      u.s = s;
+      if (s >= ns) return;
+      const Segment& z = seg[s];
+      u.tile = uni(z.tile0);
+      u.tile1 = uni(z.tile1);
+      u.c = uni(z.x.c);
+      u.nctx = (u.c + kStreamRows - 1) / kStreamRows;
+      u.p0 = uni(z.x.p0);
+      u.p1 = uni(z.x.p1);
+      u.seq = uni(z.x.seq);
+      u.grp = uni(z.x.grp);
+      u.head = uni(z.set * kWaves + wave);
+    };
+    auto step = [&](Cursor& u) __attribute__((always_inline)) {
+      if (u.s < ns && ++u.tile >= u.tile1) enter(u, u.s + 1);
+    };
+    auto find = [&](const Cursor& u) __attribute__((always_inline)) -> int2 {
+      if (u.tile < u.nctx) return make_int2(min(u.tile * kStreamRows + (lane & 31), u.c - 1), 0);
+      if (u.p1 <= u.p0) return make_int2(0, 0);
+      const int32_t r = u.p0 + (u.tile - u.nctx) * kLocal + lane;
+      return make_int2(page_row(a, u.seq, min(r, u.p1 - 1)), page_row(a, u.seq, min(r + 64, u.p1 - 1)));
+    };
+    // Memory tile: pk[i], pv[i] hold row 4 i + g, dims 8 j ...  Local tile: codes of row 16 i + j, dims 32 g ..,
+    // and sk[i], sv[i] their scales.  Piece q: i = 2 q and 2 q + 1.
+    u32x4 pk[8], pv[8];
+    uint32_t sk[8], sv[8];
+    auto load = [&](const Cursor& u, int2 where, int q) __attribute__((always_inline)) {
+      if (u.tile < u.nctx) {
+        const int64_t base = (ctx_row + u.grp * (int64_t)max_ctx) * kRow + u.head * kDim;
+#pragma unroll
+        for (int i = 2 * q; i < 2 * q + 2; ++i) {
+          const int64_t off = base + (int64_t)__shfl(where.x, 4 * i + g, 64) * kRow + 8 * j;
+          pk[i] = *reinterpret_cast<const u32x4*>(ctx_k + off);
+          pv[i] = *reinterpret_cast<const u32x4*>(ctx_v + off);
+        }
+      } else {
+#pragma unroll
+        for (int i = 2 * q; i < 2 * q + 2; ++i) {
+          const int32_t row = __shfl(i < 4 ? where.x : where.y, 16 * (i & 3) + j, 64);
+          const int64_t page = (int64_t)(row >> shift) * (kRow4 << shift);
+          const int32_t r = row & ((1 << shift) - 1);
+          const int64_t codes = page + codes4_at(u.head, r, shift) + 16 * g, scale = page + scales4_at(u.head, r, shift) + g;
+          pk[i] = *reinterpret_cast<const u32x4*>(page_k + codes);
+          sk[i] = page_k[scale];
+          pv[i] = *reinterpret_cast<const u32x4*>(page_v + codes);
+          sv[i] = page_v[scale];
+        }
+      }
+    };
+    auto load_all = [&](const Cursor& u, int2 where) __attribute__((always_inline)) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) load(u, where, q);
+    };
+    // rows of the cursor's tile, or more (0: none)
+    auto rows_of = [&](const Cursor& u) __attribute__((always_inline)) {
+      return u.tile < u.nctx ? u.c - u.tile * kStreamRows : max(0, u.p1 - u.p0) - (u.tile - u.nctx) * kLocal;
+    };
+    u32x4 qn[4];                                  // the next piece's columns: dims 32 g + 8 d ..
+    auto load_q = [&](int32_t s) __attribute__((always_inline)) {
+      const Column y = column_of(a, seg[s].x, layer, seg[s].set * kWaves + wave, j);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        qn[d] = u32x4{0u, 0u, 0u, 0u};
+        if (y.live) qn[d] = *reinterpret_cast<const u32x4*>(a.q + y.row * kDim + 32 * g + 8 * d);
+      }
+    };
+    // The loaded tile of cursor u; then(q) once piece q's registers have been used.
+    auto attend_tile = [&](auto care, const Cursor& u, int32_t limit, const u32x4* qf, State16& st,
+                           auto&& then) __attribute__((always_inline)) {
+      constexpr bool CAREFUL = decltype(care)::value;
+      const int32_t rows = rows_of(u);
+      f32x4 s[2];
+      if (u.tile < u.nctx) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          *reinterpret_cast<u32x4*>(tile + (4 * i + g) * kKStride + 8 * j) = pk[i];
+          if (rows < kStreamRows && 4 * i + g >= rows) pv[i] = u32x4{0u, 0u, 0u, 0u};   // copies of the last row: weight 0
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+            s[i] = mfma16(*reinterpret_cast<const u32x4*>(tile + (16 * i + j) * kKStride + 32 * g + 8 * d), qf[d], s[i]);
+        }
+        // the wave's LDS accesses complete in order: the V rows may follow the reads
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<u32x4*>(tile + (4 * i + g) * kVStride + 8 * j) = pv[i];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) then(q);
+        attend_scored<PARTS, CAREFUL>(tile, s, rows, a.scale2, lane, st);
+      } else {
+        const int32_t left = min(rows, limit - (u.tile - u.nctx) * kLocal);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const bool some = q == 0 || 32 * q < rows;          // uniform
+          if (some) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float k = scale4(sk[2 * q + i]), v = scale4(sv[2 * q + i]);
+              s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int d = 0; d < 4; ++d) {
+                s[i] = mfma16(values4(pk[2 * q + i][d], k), qf[d], s[i]);
+                *reinterpret_cast<u32x4*>(tile + (16 * i + j) * kVStride + 32 * g + 8 * d) = values4(pv[2 * q + i][d], v);
+              }
+            }
+          }
+          then(q);
+          if (some) attend_scored<PARTS, CAREFUL>(tile, s, left - 32 * q, a.scale2, lane, st);
+        }
+      }
+    };
+    enter(l, 0);
+    w = l;
+    int2 where = make_int2(0, 0);
+    if (l.s < ns) {
+      load_all(l, find(l));
+      load_q(0);
+      step(w);
+      if (w.s < ns) where = find(w);
+    }
+    x = w;
+    step(x);
+    while (l.s < ns) {
+      const int32_t s = l.s;
+      // first local row (from p0) that the column does not see
+      int32_t limit = 0;
+      if (seg[s].x.p1 > seg[s].x.p0) {
+        const Column y = column_of(a, seg[s].x, layer, 0, j);
+        limit = seg[s].limit0 + (y.t - seg[s].x.t0);
+        if (seg[s].x.shared && y.live) {
+          int32_t lo = 0, hi = a.B - 1;           // the token's sequence
+          while (lo < hi) {
+            const int32_t mid = (lo + hi) >> 1;
+            if (a.q_off[mid + 1] <= y.t) lo = mid + 1;
+            else hi = mid;
+          }
+          limit = visible_rows(a.kv_len[lo], a.q_off[lo + 1], y.t);
+        }
+      }
+      u32x4 qf[4];
+#pragma unroll
+      for (int d = 0; d < 4; ++d) qf[d] = qn[d];
+      State16 st;
+      clear(st);
+      while (l.s == s) {
+        // looked up before the next tile's loads: what is waited for first comes first
+        int2 after = where;
+        if (x.s < ns) after = find(x);
+        attend_tile(std::false_type(), l, limit, qf, st, [&](int q) __attribute__((always_inline)) {
+          if (w.s < ns) {
+            load(w, where, q);
+            if (q == 3 && w.s != s) load_q(w.s);
+          }
+        });
+        l = w;
+        w = x;
+        where = after;
+        step(x);
+      }
+      if (needs_care(st)) {
+        clear(st);
+        Cursor u = l;
+        enter(u, s);
+        for (; u.tile < u.tile1; ++u.tile) {
+          load_all(u, find(u));
+          attend_tile(std::true_type(), u, limit, qf, st, [](int) {});
+        }
+        if (l.s < ns) load_all(l, find(l));       // the next piece's first tile again
+      }
+      const Job job = seg[s].x;
+      const Column y = column_of(a, job, layer, seg[s].set * kWaves + wave, j);
+      if (seg[s].first && wave == 0 && y.live && g == 0 && (j & (a.G - 1)) == 0)
+        describe(a, job, y, layer, seg[s].parts, 0, 1, kWaves, j);
+      const int32_t slot = uni(seg[s].slot);
+      write_state<BF16_OUT>(a, st, rows4_sum(st.l), y, layer, slot < 0 ? -1 : kWaves * slot + wave, lane);
+    }
+    if (reached == 0) return;                     // uniform
+    from = reached;
+    __syncthreads();
+    load_lengths(a, n, layer, tid);
+    p = plan_of<Rows4>(a, n, layer, tid);
+  }
+}
+
+// ------------------------------------------------------------------ more columns
+
+// An item: four tiles a step, brought to the four stages, then used.
+template <bool BF16_OUT>
+__device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& n, ItemShared& z, u32x4* stage0, u32x4* stage1,
+                                            u32x4* stage2, u32x4* stage3, int64_t layer, int tid) {
+  constexpr int PARTS = BF16_OUT ? 1 : 3;
+  const int lane = tid & 63, wave = tid >> 6;
+  const int c = lane & 31, h = lane >> 5;
+  const Item& it = z.item;
+  auto uni = [](int32_t v) { return __builtin_amdgcn_readfirstlane(v); };
+  const Job x = it.x;
+  // fewer column blocks than waves: `share` waves take a block's columns and the tiles in turn
+  const int32_t blocks = uni(it.blocks), unit = uni(it.unit), share = kWaves / blocks;
+  const int32_t tile0 = uni(it.tile0), head = uni(it.head);
+  int32_t tile1 = uni(it.tile1);
+  const int cb = wave & (blocks - 1), turn = uni(wave / blocks);
+  const Column y = column_of(a, x, layer, head, it.col0 + cb * kCols + c);
+  int32_t limit = 0;                                 // first local row (from p0) the column does not see
+  if (y.live && x.p1 > x.p0) {
+    const int32_t b = x.shared ? min(count_upto(n.off, a.B, y.t), a.B - 1) : x.seq;
+    limit = clampi(visible_rows(n.len[b], n.off[b + 1], y.t) - x.p0, 0, x.p1 - x.p0);
+  }
+  int32_t most = limit, least = y.live ? limit : 0x7FFFFFFF;
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) {
+    most = max(most, __shfl_xor(most, off, 64));
+    least = min(least, __shfl_xor(least, off, 64));
+  }
+  most = uni(most);
+  least = uni(least);
+  u32x4 qf[8];
+#pragma unroll
+  for (int d = 0; d < 8; ++d) {
+    qf[d] = u32x4{0u, 0u, 0u, 0u};
+    if (y.live) qf[d] = *reinterpret_cast<const u32x4*>(a.q + y.row * kDim + 16 * d + 8 * h);
+  }
+  if (it.first && turn == 0 && y.live && h == 0 && (c & (a.G - 1)) == 0)
+    describe(a, x, y, layer, it.parts, it.unit < 0 ? 0 : kBlockUnits * cb, it.width, it.width * kHeads, c);
+  if (lane == 0) z.most[wave] = most;
+  __syncthreads();                                   // the lengths' memory becomes the tiles'
+
+  const int32_t jc = uni(x.c), p0 = uni(x.p0), seq = uni(x.seq), nctx = (jc + kTileRows - 1) / kTileRows;
+  int32_t wg_most = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) wg_most = max(wg_most, z.most[w]);
+  wg_most = uni(wg_most);
+  tile1 = min(tile1, nctx + (wg_most + kTileRows - 1) / kTileRows);
+
+  const int64_t ctx_at = (layer * a.n_groups + uni(x.grp)) * (int64_t)a.max_ctx * kRow + head * kDim;
+  const int64_t layer_at = ((layer * a.n_pages) << a.page_shift) * kRow4;
+  const uint16_t *ctx_k = a.ctx_k + ctx_at, *ctx_v = a.ctx_v + ctx_at;
+  const int32_t shift = kept(a.page_shift);
+  // a local tile's blocks, one a thread: waves 0 and 1 K, 2 and 3 V; row br of the tile, dims 32 bb ..
+  const uint8_t* pages = (const uint8_t*)(wave < 2 ? a.k_pages : a.v_pages) + layer_at;
+  const int br = 16 * (wave & 1) + (lane >> 2), bb = lane & 3;
+  // where its chunk d lies in a stage: chunk 4 bb + d permuted as the reads expect
+  const int lds_row = (wave < 2 ? 0 : kTileRows * 16) + br * 16 + 4 * (bb ^ (wave < 2 ? (br >> 2) & 3 : br & 3));
+  auto fill_local = [&](int32_t t, u32x4* stage) __attribute__((always_inline)) {
+    const int32_t row = page_row(a, seq, p0 + min((t - nctx) * kTileRows + br, wg_most - 1));
+    const int32_t r = row & ((1 << shift) - 1);
+    const uint8_t* page = pages + (int64_t)(row >> shift) * (kRow4 << shift);
+    const u32x4 raw = *reinterpret_cast<const u32x4*>(page + codes4_at(head, r, shift) + 16 * bb);
+    const float s = scale4(page[scales4_at(head, r, shift) + bb]);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) stage[lds_row + (d ^ (br & 3))] = values4(raw[d], s);
+  };
+  auto fill_ctx = [&](int32_t t, u32x4* stage) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 8 * wave + 4 * i + (lane >> 4);
+      const int64_t at = (int64_t)min(t * kTileRows + r, jc - 1) * kRow;
+      u32x4* to = stage + 16 * (8 * wave + 4 * i);
+      __builtin_amdgcn_global_load_lds((gptr_t)(ctx_k + at + 8 * ((lane & 15) ^ (r & 15))), (lptr_t)to, 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((gptr_t)(ctx_v + at + 8 * ((lane & 15) ^ (5 * (r & 3)))),
+                                       (lptr_t)(to + kTileRows * 16), 16, 0, 0);
+    }
+  };
+  auto fill = [&](int32_t t, u32x4* stage) __attribute__((always_inline)) {
+    if (t < nctx) fill_ctx(t, stage);
+    else fill_local(t, stage);
+  };
+  const StageReads at(lane);
+  State st;
+  clear(st);
+  // rows of tile t that a column sees, or more; whether all the wave's columns see all of it
+  auto left_of = [&](int32_t t) __attribute__((always_inline)) {
+    return t >= tile1 ? 0 : (t < nctx ? jc - t * kTileRows : limit - (t - nctx) * kTileRows);
+  };
+  const int32_t odd = jc & (kTileRows - 1) ? nctx - 1 : -1, whole_end = nctx + min(wg_most, least) / kTileRows;
+  auto whole = [&](int32_t t) __attribute__((always_inline)) { return t != odd && t < whole_end; };
+  const int32_t last = tile1 - 1;
+  auto pass = [&](auto care) __attribute__((always_inline)) {
+    constexpr bool CAREFUL = decltype(care)::value;
+    const uint32_t a0 = lds_at(stage0), a1 = lds_at(stage1), a2 = lds_at(stage2), a3 = lds_at(stage3);
+#pragma unroll 1
+    for (int32_t t = tile0; t < tile1; t += 4) {
+      fill(t, stage0);
+      fill(min(t + 1, last), stage1);
+      fill(min(t + 2, last), stage2);
+      fill(min(t + 3, last), stage3);
+      __builtin_amdgcn_s_waitcnt(0x70);           // vmcnt, lgkmcnt 0
+      __syncthreads();
+#pragma unroll 1
+      for (int i = turn; i < 4; i += share) {
+        if (t + i >= tile1) break;
+        const u32x4* s = lds_ptr(i == 0 ? a0 : (i == 1 ? a1 : (i == 2 ? a2 : a3)));
+        attend_tiles<PARTS, CAREFUL, 1>(nullptr, s, s, at, qf, t + i, whole(t + i), left_of, a.scale2, h, st);
+      }
+      __syncthreads();
+    }
+  };
+  pass(std::false_type());
+  if (__syncthreads_or(needs_care(st))) {
+    clear(st);
+    pass(std::true_type());
+  }
+  finish_item<BF16_OUT>(a, z, st, y, layer, unit, blocks, cb, turn, wave, lane, stage1, stage2, stage3);
+}
+
+template <bool BF16_OUT>
+__global__ void __launch_bounds__(kThreads, 2)
+attend4_kernel(const AttendArgs a) {
+  __shared__ u32x4 stage0[kStage], stage1[kStage], stage2[kStage], stage3[kStage];
+  __shared__ union {
+    ItemShared item;
+    struct {
+      Segment seg[kSegments];
+      uint32_t n_seg[3];
+    } streams;
+  } sh;
+  const int tid = threadIdx.x;
+  // layers fastest: the workgroups that turn out to have nothing to do come last
+  const int64_t layer = blockIdx.x;
+  const uint32_t id = blockIdx.z * gridDim.y + blockIdx.y;
+  if (a.plans && id >= a.plans[layer * kThreads].shares + a.plans[layer * kThreads].all_items) return;
+  Lengths n = lengths_in(stage0, stage1, stage2, stage3);
+  load_lengths(a, n, layer, tid);
+  const Plan p = plan_of<Rows4>(a, n, layer, tid);
+  // items that fit the chip at once are the longer ones; items of many rounds end more evenly than shares
+  const bool items_first = p.all_items <= (uint32_t)a.both_wgs;
+  const uint32_t first_share = items_first ? p.all_items : 0, first_item = items_first ? 0 : p.shares;
+  if (id >= first_share && id < first_share + p.shares) {      // uniform
+    const int wave = tid >> 6;
+    u32x4* tile = wave == 0 ? stage0 : (wave == 1 ? stage1 : (wave == 2 ? stage2 : stage3));
+    attend_streams<BF16_OUT>(a, n, p, sh.streams.seg, sh.streams.n_seg, reinterpret_cast<uint16_t*>(tile),
+                             id - first_share, layer, tid);
+  } else if (id >= first_item && id < first_item + p.all_items) {
+    find_item(a, n, p, sh.item.item, id - first_item, tid);
+    if (sh.item.item.valid) attend_item<BF16_OUT>(a, n, sh.item, stage0, stage1, stage2, stage3, layer, tid);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_attend4(int32_t L, int32_t B, int32_t n_groups, int32_t n_q, int32_t Hq, const uint16_t* q,
+                          const int32_t* q_off, const int32_t* grp_off, const uint16_t* ctx_k, const uint16_t* ctx_v,
+                          const int32_t* ctx_len, int32_t max_ctx, const uint8_t* k_pages, const uint8_t* v_pages,
+                          int32_t n_pages, int32_t page_shift, const int32_t* page_table, int32_t max_pages,
+                          const int32_t* kv_len, const int32_t* pre_len, float scale, bool bf16_out, void* out,
+                          void* ws, hipStream_t s) {
+  if (!can_share(B)) grp_off = nullptr;      // one sequence, so one group
+  const Sizes z = sizes_of(L, B, n_groups, n_q, Hq / kHeads, grp_off != nullptr);
+  const AttendArgs a = args_of(z, B, n_groups, n_q, Hq, q, q_off, grp_off, ctx_k, ctx_v, ctx_len, max_ctx, k_pages, v_pages,
+                               n_pages, page_shift, page_table, max_pages, kv_len, pre_len, scale, out, ws);
+  if (bf16_out) launch_as<Rows4, true>(attend4_kernel<true>, a, z, L, s);
+  else launch_as<Rows4, false>(attend4_kernel<false>, a, z, L, s);
+  return hipGetLastError();
+}
+
+}  // namespace msa

@@ -775,6 +775,29 @@ __device__ __forceinline__ void find_item(const AttendArgs& a, const Lengths& n,
 
 // ------------------------------------------------------------------ tiles of up to 16 columns
 
+// 32 rows whose scores are formed (rows 16 kb + 4 g + r of column j in s[kb][r]) and whose V rows lie in the wave's tile.
+template <int PARTS, bool CAREFUL>
+__device__ __forceinline__ void attend_scored(const uint16_t* tile, const f32x4* s, int32_t left, float scale2, int lane,
+                                              State16& st) {
+  const int j = lane & 15, g = lane >> 4;
+  // probabilities as the B operand: k slot 8 g + e holds row 4 g + e (e < 4) or 16 + 4 g + e - 4
+  float v[8], mt = -__builtin_huge_valf();
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    v[e] = 16 * (e >> 2) + 4 * g + (e & 3) < left ? s[e >> 2][e & 3] : -__builtin_huge_valf();
+    mt = fmaxf(mt, v[e]);
+  }
+  raise_to<CAREFUL>(rows4_max(mt), scale2, st);
+  u32x4 pw[PARTS];
+  weights<PARTS, CAREFUL>(v, scale2, st.neg, pw, st.l);
+  // a 16-lane group reads 16 dims of 4 rows transposed
+  const uint16_t* vsrc = tile + (4 * g + (j >> 2)) * kVStride + 4 * (j & 3);
+#pragma unroll
+  for (int d = 0; d < 8; ++d)
+    add_values<PARTS, CAREFUL>(frag_of(lds_read_tr16(vsrc + 16 * d), lds_read_tr16(vsrc + 16 * kVStride + 16 * d)), pw,
+                               st.o[d]);
+}
+
 // 32 rows in the wave's tile: K rows while the scores are formed, then V rows; `then` once these are in.
 template <int PARTS, bool CAREFUL, typename Then>
 __device__ __forceinline__ void attend_rows(uint16_t* tile, const u32x4* pv, const u32x4* qf, int32_t left, float scale2,
@@ -793,32 +816,17 @@ __device__ __forceinline__ void attend_rows(uint16_t* tile, const u32x4* pv, con
   for (int i = 0; i < 8; ++i)
     *reinterpret_cast<u32x4*>(tile + (4 * i + g) * kVStride + 8 * j) = pv[i];
   then();
-  // rows 16 kb + 4 g + r; probabilities as the B operand: k slot 8 g + e holds row 4 g + e (e < 4) or
-  // 16 + 4 g + e - 4
-  float v[8], mt = -__builtin_huge_valf();
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    v[e] = 16 * (e >> 2) + 4 * g + (e & 3) < left ? s[e >> 2][e & 3] : -__builtin_huge_valf();
-    mt = fmaxf(mt, v[e]);
-  }
-  raise_to<CAREFUL>(rows4_max(mt), scale2, st);
-  u32x4 pw[PARTS];
-  weights<PARTS, CAREFUL>(v, scale2, st.neg, pw, st.l);
-  // a 16-lane group reads 16 dims of 4 rows transposed
-  const uint16_t* vsrc = tile + (4 * g + (j >> 2)) * kVStride + 4 * (j & 3);
-#pragma unroll
-  for (int d = 0; d < 8; ++d)
-    add_values<PARTS, CAREFUL>(frag_of(lds_read_tr16(vsrc + 16 * d), lds_read_tr16(vsrc + 16 * kVStride + 16 * d)), pw,
-                               st.o[d]);
+  attend_scored<PARTS, CAREFUL>(tile, s, left, scale2, lane, st);
 }
 
 // ------------------------------------------------------------------ tiles of more columns
 
 // A stage holds 32 K rows, then 32 V rows, 16 chunks of 16 bytes each, as the direct
 // global -> LDS loads write them: lane l of load i brings chunk (l & 15) of row 4 i + (l >> 4).  The
-// chunks of a row are permuted by the lanes' source addresses, so that fragment reads meet every bank
+// chunks of a row are permuted (bf16 rows: by the lanes' source addresses), so that fragment reads meet every bank
 // once: chunk x of K row r lies at x ^ (r & 15) (16 rows, one chunk each), of V row r at
-// x ^ 4 (r & 3) (4 rows, 4 chunks each).
+// x ^ 5 (r & 3) (4 rows, 4 chunks each).  16 lanes that write a chunk of four rows' four blocks of 32 dims meet
+// every bank once as well.
 static_assert(kStage == 2 * kTileRows * 16, "K rows and V rows");
 
 typedef __attribute__((address_space(1))) const void* gptr_t;
@@ -843,7 +851,7 @@ struct StageReads {
     }
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-      const int x = 4 * (d ^ (i >> 2)) + 2 * ((lane >> 4) & 1) + ((i >> 1) & 1);
+      const int x = 4 * (d ^ (i >> 2)) + ((2 * ((lane >> 4) & 1) + ((i >> 1) & 1)) ^ (i >> 2));
       vb[d] = 2 * ((kTileRows + 4 * h + (i >> 2)) * kDim + 8 * x + 4 * (i & 1));
       asm("" : "+v"(vb[d]));
     }

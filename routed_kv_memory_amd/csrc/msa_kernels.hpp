@@ -83,4 +83,12 @@ hipError_t launch_attend(int32_t L, int32_t B, int32_t n_groups, int32_t n_q, in
                          const int32_t* kv_len, const int32_t* pre_len, float scale, bool bf16_out, void* out,
                          void* ws, hipStream_t s);
 
+// attend4.hip; its workspace is attend_workspace_bytes
+hipError_t launch_attend4(int32_t L, int32_t B, int32_t n_groups, int32_t n_q, int32_t Hq, const uint16_t* q,
+                          const int32_t* q_off, const int32_t* grp_off, const uint16_t* ctx_k, const uint16_t* ctx_v,
+                          const int32_t* ctx_len, int32_t max_ctx, const uint8_t* k_pages, const uint8_t* v_pages,
+                          int32_t n_pages, int32_t page_shift, const int32_t* page_table, int32_t max_pages,
+                          const int32_t* kv_len, const int32_t* pre_len, float scale, bool bf16_out, void* out,
+                          void* ws, hipStream_t s);
+
 }  // namespace msa

@@ -61,6 +61,9 @@ _SIGS = {
                           _P, _F32, _I32, _P, _P, _SZ, _P], ctypes.c_int),
     "msa_paged_append4": ([_I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _F32, _F32, _P,
                            _P, _P, _P], ctypes.c_int),
+    "msa_paged_attend4_workspace_size": ([_I32, _I32, _I32, _I32, _I32], _SZ),
+    "msa_paged_attend4": ([_I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _P, _I32, _P,
+                           _P, _F32, _I32, _P, _P, _SZ, _P], ctypes.c_int),
     "msa_paged_read4": ([_I32, _I32, _I32, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _P, _P], ctypes.c_int),
 }
 
@@ -484,3 +487,36 @@ def msa_paged_read4(k_pages, v_pages, row_off, page_table, k_out, v_out, row0=No
         _on(dev, page_table, _I32T, None, "page_table"), max_pages, page_tokens, n_pages,
         _on(dev, k_pages, _U8, None, "k_pages"), _on(dev, v_pages, _U8, p_shape, "v_pages"),
         _on(dev, k_out, _BF16, rows, "k_out", o_shape), _on(dev, v_out, _BF16, rows, "v_out")))
+
+
+def msa_paged_attend4_workspace_size(n_layers, B, n_groups, n_q, Hq) -> int:
+    return int(lib().msa_paged_attend4_workspace_size(n_layers, B, n_groups, n_q, Hq))
+
+
+def msa_paged_attend4(q, q_off, kv_len, page_table, k_pages, v_pages, scale, out, workspace, grp_off=None, ctx_k=None,
+                      ctx_v=None, ctx_len=None, pre_len=None, stream=None):
+    """msa_paged_attend over pages in 4 bits (k_pages, v_pages as for msa_paged_append4); the other arguments as
+    there."""
+    q_shape = _dims(q, 4, "q")
+    L, n_q, Hq = q_shape[0], q_shape[1], q_shape[2]
+    p_shape, n_pages, page_tokens = _pages4(k_pages)
+    B, max_pages = _dims(page_table, 2, "page_table")
+    o_shape = _dims(out, 4, "out")
+    _required(q_off=q_off, kv_len=kv_len, v_pages=v_pages, workspace=workspace)
+    n_groups = B if grp_off is None else _dims(grp_off, 1, "grp_off")[0] - 1
+    if ctx_k is None:
+        max_ctx, ctx_v, ctx_len = 0, None, None
+    else:
+        max_ctx = _dims(ctx_k, 5, "ctx_k")[2]
+        _required(ctx_v=ctx_v, ctx_len=ctx_len)
+    dev = q.get_device()
+    heads, pages, ctx = (L, n_q, Hq, HEAD_DIM), (L, n_pages, p_shape[2]), (L, n_groups, max_ctx, HEADS, HEAD_DIM)
+    _call("msa_paged_attend4", dev, stream, (
+        L, B, n_groups, n_q, Hq, _on(dev, q, _BF16, heads, "q", q_shape), _on(dev, q_off, _I32T, (B + 1,), "q_off"),
+        _on(dev, grp_off, _I32T, None, "grp_off"), _on(dev, ctx_k, _BF16, ctx, "ctx_k"),
+        _on(dev, ctx_v, _BF16, ctx, "ctx_v"), _on(dev, ctx_len, _I32T, (L, n_groups), "ctx_len"), max_ctx,
+        _on(dev, k_pages, _U8, pages, "k_pages", p_shape), _on(dev, v_pages, _U8, pages, "v_pages"), n_pages, page_tokens,
+        _on(dev, page_table, _I32T, None, "page_table"), max_pages, _on(dev, kv_len, _I32T, (B,), "kv_len"),
+        _on(dev, pre_len, _I32T, (n_groups,), "pre_len"), float(scale), 0 if out.dtype == torch.float32 else 1,
+        _on(dev, out, _F32_BF16, heads, "out", o_shape), _on(dev, workspace, _ANY, None, "workspace"),
+        workspace.numel() * workspace.element_size()))

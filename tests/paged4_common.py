@@ -2,7 +2,8 @@
 definition, and batches whose pages hold it."""
 import torch
 
-from paged_common import Batch
+from paged_common import SCALE, Batch
+from paged_exact import attend64
 
 ROW4 = 544
 ELEMENTS = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64)
@@ -16,6 +17,9 @@ def exponents(m):
 
 def quantise(x):
     """Rows x [..., 128] in 64 bits: codes [..., 128] and scale bytes [..., 4]."""
+    if x.numel() > 1 << 22 and x.dim() > 1:        # in pieces: the distances take 64 bytes a value
+        parts = [quantise(p) for p in x.flatten(0, -2).split(1 << 15)]
+        return tuple(torch.cat([p[i] for p in parts]).view(*x.shape[:-1], -1) for i in range(2))
     b = x.double().unflatten(-1, (4, 32))
     odd = ~torch.isfinite(b).all(-1)
     b = torch.where(odd[..., None], 0.0, b)
@@ -62,11 +66,45 @@ class Batch4(Batch):
             self.hold(name, getattr(self, name))
 
     def hold(self, name, rows):
-        codes, scales = quantise(rows)
-        setattr(self, name + "4", pack(codes, scales))
-        setattr(self, name, values(codes, scales).to(torch.bfloat16))
+        codes, scales = quantise(rows.to(self.device))
+        setattr(self, name + "4", pack(codes, scales).cpu())
+        setattr(self, name, values(codes, scales).to(torch.bfloat16).cpu())
 
     def to_device(self):
         d = super().to_device()
         d["k_pages"], d["v_pages"] = self.k_pages4.to(self.device), self.v_pages4.to(self.device)
         return d
+
+
+def check_every_token(out, q, q_off, kv_len, table, k_pages, v_pages, ctx=None, scale=SCALE):
+    """All of out [L][n_q][hq][128] over rows [L][n_pages][P][8][128] of the values that are held.  q_off, kv_len: lists;
+    ctx: (ctx_k, ctx_v [L][G][max_ctx][8][128], their lengths [layer][group], group of each sequence) or None.
+
+    The bound is attend64's, and 2^-126 (1 + r max|v|) for r rows: many held values are 0, so an output may be a sum of weights near
+    fp32's smallest normal number alone; a weight below that comes out as 0, and so may an output."""
+    L, page, dev = out.shape[0], k_pages.shape[2], out.device
+    worst, at = [], []
+    for b, rows in enumerate(kv_len):
+        n = q_off[b + 1] - q_off[b]
+        if n == 0:
+            continue
+        r = torch.arange(max(rows, 0), device=dev)
+        where = table[b].long()[r // page]
+        k, v = k_pages[:, where, r % page], v_pages[:, where, r % page]
+        seen = (r[None] <= rows - n + torch.arange(n, device=dev)[:, None]).expand(L, n, -1)
+        if ctx is not None:
+            ck, cv, lens, group = ctx
+            c = torch.tensor([x[group[b]] for x in lens], device=dev)
+            most = int(max(x[group[b]] for x in lens))
+            k, v = (torch.cat([t[:, group[b], :most], y], 1) for t, y in ((ck, k), (cv, v)))
+            mem = torch.arange(most, device=dev)[None] < c[:, None]
+            seen = torch.cat([mem[:, None].expand(L, n, most), seen], 2)
+        mine = slice(q_off[b], q_off[b + 1])
+        ref, tol = attend64(q[:, mine], k, v, seen, scale, out.dtype)
+        if k.shape[1]:
+            tol = tol + 2.0 ** -126 * (1 + k.shape[1] * v.double().abs().amax())
+        worst.append(((out[:, mine].double() - ref).abs() - tol).flatten(1).amax(1))   # not a number: stays one
+        at += [(l, b) for l in range(L)]
+    worst = torch.cat(worst).cpu().tolist()
+    wrong = [(x, w) for x, w in zip(at, worst) if not w <= 0]
+    assert not wrong, "%d of %d (layer, sequence) pairs are over their bound: %s" % (len(wrong), len(at), wrong[:6])

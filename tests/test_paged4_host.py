@@ -36,6 +36,16 @@ def read(msa, **change):
     return msa.lib().msa_paged_read4(*a.values())
 
 
+def attend(msa, **change):
+    a = dict(n_layers=1, B=2, n_groups=2, n_q=3, Hq=32, q=fake, q_off=fake, grp_off=None, ctx_k=None, ctx_v=None,
+             ctx_len=None, max_ctx=0, k_pages=fake, v_pages=fake, n_pages=9, page_tokens=16, page_table=fake,
+             max_pages=4, kv_len=fake, pre_len=None, scale=F(0.1), out_bf16=0, out=fake, workspace=fake,
+             workspace_bytes=1 << 40, stream=None)
+    assert set(change) <= set(a)
+    a.update(change)
+    return msa.lib().msa_paged_attend4(*a.values())
+
+
 SIZES = [
     (SHAPE, dict(n_layers=0)), (SHAPE, dict(B=0)), (SHAPE, dict(max_pages=0)), (SHAPE, dict(n_pages=0)),
     (SHAPE, dict(page_tokens=0)), (SHAPE, dict(page_tokens=24)), (SHAPE, dict(page_tokens=2048)),
@@ -68,10 +78,34 @@ def test_read_refuses(msa, status, change):
     assert msa.lib().msa_last_error().startswith(b"msa_paged_read4")
 
 
+@pytest.mark.parametrize("status,change", [
+    (st, ch) for st, ch in SIZES if "B" not in ch] + [
+    (SHAPE, dict(B=0)), (UNSUPPORTED, dict(B=2049, n_groups=1, grp_off=fake)),
+    (NULL, dict(q=None)), (NULL, dict(q_off=None)), (NULL, dict(kv_len=None)), (NULL, dict(out=None)),
+    (NULL, dict(workspace=None)), (NULL, dict(max_ctx=8)), (NULL, dict(max_ctx=8, ctx_k=fake, ctx_v=fake)),
+    (NULL, dict(n_groups=1)), (SHAPE, dict(q=odd)), (SHAPE, dict(out=odd)),
+    (SHAPE, dict(max_ctx=8, ctx_k=odd, ctx_v=fake, ctx_len=fake)), (SHAPE, dict(n_groups=0)), (SHAPE, dict(n_groups=3)),
+    (SHAPE, dict(n_q=-1)), (SHAPE, dict(max_ctx=-1)), (SHAPE, dict(Hq=20)), (UNSUPPORTED, dict(Hq=40)),
+    (SHAPE, dict(scale=F(0.0))), (SHAPE, dict(scale=F(float("nan")))), (SHAPE, dict(scale=F(float("inf")))),
+    (SHAPE, dict(out_bf16=2)), (UNSUPPORTED, dict(n_q=(1 << 22) + 1)), (WORKSPACE, dict(workspace_bytes=16)),
+])
+def test_attend_refuses(msa, status, change):
+    assert attend(msa, **change) == status
+    assert msa.lib().msa_last_error().startswith(b"msa_paged_attend4")
+
+
+def test_attend_workspace(msa):
+    size = msa.msa_paged_attend4_workspace_size
+    assert size(18, 16, 1, 16, 32) > 0 and size(18, 16, 1, 16, 32) == msa.msa_paged_attend_workspace_size(18, 16, 1, 16, 32)
+    assert size(1, 2, 3, 1, 32) == size(1, 0, 1, 1, 32) == size(1, 1, 1, 1, 24) == 0
+    assert attend(msa, workspace_bytes=size(1, 2, 2, 3, 32) - 1) == WORKSPACE
+
+
 def test_no_rows_enqueue_nothing(msa):
     assert append(msa, n_q=0, k_new=None, v_new=None, q=None, q_out=None) == OK
     assert append(msa, n_q=0, theta=F(0.0)) == OK
     assert read(msa, n_rows=0, k_out=None, v_out=None) == OK
+    assert attend(msa, n_q=0, q=None, out=None) == OK
 
 
 def test_the_binding_refuses(msa):
