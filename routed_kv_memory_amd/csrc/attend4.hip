@@ -15,7 +15,7 @@ namespace msa {
 namespace {
 
 struct Rows4 {
-  static constexpr int kStreamLocal = 128;
+  static constexpr int kStreamCtx = 16, kStreamLocal = 64;
 };
 
 // A share of the streams; `tile` is the wave's.
@@ -23,18 +23,22 @@ template <bool BF16_OUT>
 __device__ __forceinline__ void attend_streams(const AttendArgs& a, Lengths& n, Plan p, Segment* seg, uint32_t* n_seg,
                                                uint16_t* tile, uint32_t number, int64_t layer, int tid) {
   constexpr int PARTS = BF16_OUT ? 1 : 3;
-  constexpr int kLocal = Rows4::kStreamLocal;
-  static_assert(kLocal == 128, "two rows a lane are found, four pieces of 32 used");
-  static_assert(kStage * 16 >= kStreamRows * kVStride * 2, "a stage holds a wave's tile");
+  constexpr int kCtx = Rows4::kStreamCtx, kLocal = Rows4::kStreamLocal;
+  static_assert(kCtx == 16 && kLocal == 64, "either fits 4 loads of K and of V a lane");
   const int lane = tid & 63, wave = tid >> 6;
   const int j = lane & 15, g = lane >> 4;
   auto uni = [](int32_t v) { return __builtin_amdgcn_readfirstlane(v); };
+  // a local tile's V: codes as they were loaded, and 32 rows at a time turned into bf16
+  constexpr int kRawBytes = kLocal * kCodes4, kTileAt = kStage * 16 - 32 * kVStride * 2;
+  static_assert(kTileAt >= kRawBytes && kTileAt % 16 == 0, "both fit a stage");
+  u32x4* raw = reinterpret_cast<u32x4*>(tile);
+  uint16_t* vtile = tile + kTileAt / 2;
 
-  const uint16_t *ctx_k = kept(a.ctx_k), *ctx_v = kept(a.ctx_v);
   const int32_t max_ctx = kept(a.max_ctx), shift = kept(a.page_shift);
+  const char *ctx_k = kept((const char*)a.ctx_k), *ctx_v = kept((const char*)a.ctx_v);
   const int64_t ctx_row = kept(layer * a.n_groups * (int64_t)a.max_ctx);
   const int64_t layer_at = ((layer * a.n_pages) << shift) * kRow4;
-  const uint8_t *page_k = kept((const uint8_t*)a.k_pages + layer_at), *page_v = kept((const uint8_t*)a.v_pages + layer_at);
+  const char *page_k = kept((const char*)a.k_pages + layer_at), *page_v = kept((const char*)a.v_pages + layer_at);
 
   for (uint32_t from = 0;;) {
     if (tid < 3) n_seg[tid] = 0;
@@ -43,11 +47,11 @@ __device__ __forceinline__ void attend_streams(const AttendArgs& a, Lengths& n, 
     const int32_t ns = uni((int32_t)n_seg[0]);
     __syncthreads();                              // the lengths' memory becomes the tiles'
 
-    // Three cursors across the pieces: `l` is used; `w` is loaded, piece by piece into the registers that l's rows
-    // leave; the rows of `x` are looked up (lane r the r-th and the 64 + r-th of the tile).
+    // Two cursors run ahead of the tile that is used, across the pieces: `w` finds rows (lane r the r-th
+    // of the tile), one tile later they are loaded, one tile later used.
     struct Cursor {
       int32_t s, tile, tile1, nctx, c, p0, p1, seq, grp, head;
-    } l, w, x;
+    } w, l;
     auto enter = [&](Cursor& u, int32_t s) __attribute__((always_inline)) {
       u.s = s;
       if (s >= ns) return;
@@ -55,7 +59,7 @@ __device__ __forceinline__ void attend_streams(const AttendArgs& a, Lengths& n, 
       u.tile = uni(z.tile0);
       u.tile1 = uni(z.tile1);
       u.c = uni(z.x.c);
-      u.nctx = (u.c + kStreamRows - 1) / kStreamRows;
+      u.nctx = (u.c + kCtx - 1) / kCtx;
       u.p0 = uni(z.x.p0);
       u.p1 = uni(z.x.p1);
       u.seq = uni(z.x.seq);
@@ -63,48 +67,37 @@ __device__ __forceinline__ void attend_streams(const AttendArgs& a, Lengths& n, 
       u.head = uni(z.set * kWaves + wave);
     };
     auto step = [&](Cursor& u) __attribute__((always_inline)) {
-      if (u.s < ns && ++u.tile >= u.tile1) enter(u, u.s + 1);
+      if (++u.tile >= u.tile1) enter(u, u.s + 1);
     };
-    auto find = [&](const Cursor& u) __attribute__((always_inline)) -> int2 {
-      if (u.tile < u.nctx) return make_int2(min(u.tile * kStreamRows + (lane & 31), u.c - 1), 0);
-      if (u.p1 <= u.p0) return make_int2(0, 0);
-      const int32_t r = u.p0 + (u.tile - u.nctx) * kLocal + lane;
-      return make_int2(page_row(a, u.seq, min(r, u.p1 - 1)), page_row(a, u.seq, min(r + 64, u.p1 - 1)));
+    auto find = [&](const Cursor& u) __attribute__((always_inline)) -> int32_t {
+      if (u.tile < u.nctx) return min(u.tile * kCtx + j, u.c - 1);
+      return u.p1 > u.p0 ? page_row(a, u.seq, min(u.p0 + (u.tile - u.nctx) * kLocal + lane, u.p1 - 1)) : 0;
     };
     // Memory tile: pk[i], pv[i] hold row 4 i + g, dims 8 j ...  Local tile: codes of row 16 i + j, dims 32 g ..,
-    // and sk[i], sv[i] their scales.  Piece q: i = 2 q and 2 q + 1.
-    u32x4 pk[8], pv[8];
-    uint32_t sk[8], sv[8];
-    auto load = [&](const Cursor& u, int2 where, int q) __attribute__((always_inline)) {
-      if (u.tile < u.nctx) {
-        const int64_t base = (ctx_row + u.grp * (int64_t)max_ctx) * kRow + u.head * kDim;
+    // and sk[i], sv[i] their scales (of a memory tile: nothing, but loaded all the same).
+    u32x4 pk[4], pv[4];
+    uint32_t sk[4], sv[4];
+    auto load = [&](const Cursor& u, int32_t where) __attribute__((always_inline)) {
+      const bool ctx = u.tile < u.nctx;           // uniform, as all but `row`
+      const char *kb = ctx ? ctx_k : page_k, *vb = ctx ? ctx_v : page_v;
+      const int64_t base = ctx ? 2 * ((ctx_row + u.grp * (int64_t)max_ctx) * kRow + u.head * kDim) : (int64_t)(u.head * kCodes4 << shift);
+      const int64_t scales = ctx ? base : (int64_t)(kHeads * kCodes4 << shift) + (u.head * kBlocks4 << shift);
+      const int by = ctx ? 31 : shift, step_hi = ctx ? 0 : kRow4 << shift, step_lo = ctx ? 2 * kRow : kCodes4;
+      const int step_s = ctx ? 2 * kRow : kBlocks4, first = ctx ? g : j, each = ctx ? 4 : 16, at = 16 * (ctx ? j : g);
 #pragma unroll
-        for (int i = 2 * q; i < 2 * q + 2; ++i) {
-          const int64_t off = base + (int64_t)__shfl(where.x, 4 * i + g, 64) * kRow + 8 * j;
-          pk[i] = *reinterpret_cast<const u32x4*>(ctx_k + off);
-          pv[i] = *reinterpret_cast<const u32x4*>(ctx_v + off);
-        }
-      } else {
-#pragma unroll
-        for (int i = 2 * q; i < 2 * q + 2; ++i) {
-          const int32_t row = __shfl(i < 4 ? where.x : where.y, 16 * (i & 3) + j, 64);
-          const int64_t page = (int64_t)(row >> shift) * (kRow4 << shift);
-          const int32_t r = row & ((1 << shift) - 1);
-          const int64_t codes = page + codes4_at(u.head, r, shift) + 16 * g, scale = page + scales4_at(u.head, r, shift) + g;
-          pk[i] = *reinterpret_cast<const u32x4*>(page_k + codes);
-          sk[i] = page_k[scale];
-          pv[i] = *reinterpret_cast<const u32x4*>(page_v + codes);
-          sv[i] = page_v[scale];
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int32_t row = __shfl(where, each * i + first, 64);
+        const int64_t page = (int64_t)(row >> by) * step_hi;
+        const int64_t r = (int64_t)(row & (int32_t)((1u << by) - 1u));
+        pk[i] = *reinterpret_cast<const u32x4*>(kb + base + page + r * step_lo + at);
+        pv[i] = *reinterpret_cast<const u32x4*>(vb + base + page + r * step_lo + at);
+        sk[i] = *reinterpret_cast<const uint8_t*>(kb + scales + page + r * step_s + g);
+        sv[i] = *reinterpret_cast<const uint8_t*>(vb + scales + page + r * step_s + g);
       }
-    };
-    auto load_all = [&](const Cursor& u, int2 where) __attribute__((always_inline)) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) load(u, where, q);
     };
     // rows of the cursor's tile, or more (0: none)
     auto rows_of = [&](const Cursor& u) __attribute__((always_inline)) {
-      return u.tile < u.nctx ? u.c - u.tile * kStreamRows : max(0, u.p1 - u.p0) - (u.tile - u.nctx) * kLocal;
+      return u.tile < u.nctx ? u.c - u.tile * kCtx : max(0, u.p1 - u.p0) - (u.tile - u.nctx) * kLocal;
     };
     u32x4 qn[4];                                  // the next piece's columns: dims 32 g + 8 d ..
     auto load_q = [&](int32_t s) __attribute__((always_inline)) {
@@ -115,65 +108,60 @@ __device__ __forceinline__ void attend_streams(const AttendArgs& a, Lengths& n, 
         if (y.live) qn[d] = *reinterpret_cast<const u32x4*>(a.q + y.row * kDim + 32 * g + 8 * d);
       }
     };
-    // The loaded tile of cursor u; then(q) once piece q's registers have been used.
-    auto attend_tile = [&](auto care, const Cursor& u, int32_t limit, const u32x4* qf, State16& st,
+    // The loaded tile; `then` once its registers have been used.
+    auto attend_tile = [&](auto care, bool ctx, int32_t rows, int32_t left, const u32x4* qf, State16& st,
                            auto&& then) __attribute__((always_inline)) {
       constexpr bool CAREFUL = decltype(care)::value;
-      const int32_t rows = rows_of(u);
-      f32x4 s[2];
-      if (u.tile < u.nctx) {
+      f32x4 s[4];
+      uint32_t sp = 0;                            // scales of V
+      if (ctx) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           *reinterpret_cast<u32x4*>(tile + (4 * i + g) * kKStride + 8 * j) = pk[i];
-          if (rows < kStreamRows && 4 * i + g >= rows) pv[i] = u32x4{0u, 0u, 0u, 0u};   // copies of the last row: weight 0
+          if (rows < kCtx && 4 * i + g >= rows) pv[i] = u32x4{0u, 0u, 0u, 0u};     // copies of the last row: weight 0
+          *reinterpret_cast<u32x4*>(vtile + (4 * i + g) * kVStride + 8 * j) = pv[i];
         }
+        s[0] = s[1] = s[2] = s[3] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int d = 0; d < 4; ++d) s[0] = mfma16(*reinterpret_cast<const u32x4*>(tile + j * kKStride + 32 * g + 8 * d), qf[d], s[0]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
           s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int d = 0; d < 4; ++d)
-            s[i] = mfma16(*reinterpret_cast<const u32x4*>(tile + (16 * i + j) * kKStride + 32 * g + 8 * d), qf[d], s[i]);
+          for (int d = 0; d < 4; ++d) s[i] = mfma16(values4(pk[i][d], scale4(sk[i])), qf[d], s[i]);
+          raw[64 * i + lane] = pv[i];
+          sp |= sv[i] << (8 * i);
         }
-        // the wave's LDS accesses complete in order: the V rows may follow the reads
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<u32x4*>(tile + (4 * i + g) * kVStride + 8 * j) = pv[i];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) then(q);
-        attend_scored<PARTS, CAREFUL>(tile, s, rows, a.scale2, lane, st);
+      }
+      then();
+      if (ctx) {
+        attend_scored16<PARTS, CAREFUL>(vtile, s[0], left, a.scale2, lane, st);
       } else {
-        const int32_t left = min(rows, limit - (u.tile - u.nctx) * kLocal);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const bool some = q == 0 || 32 * q < rows;          // uniform
-          if (some) {
+        for (int q = 0; q < 2; ++q) {
+          if (q > 0 && rows <= 32) continue;      // uniform
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float k = scale4(sk[2 * q + i]), v = scale4(sv[2 * q + i]);
-              s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+          for (int i = 0; i < 2; ++i) {
+            const u32x4 codes = raw[64 * (2 * q + i) + lane];
+            const float f = scale4((sp >> (16 * q + 8 * i)) & 255u);
 #pragma unroll
-              for (int d = 0; d < 4; ++d) {
-                s[i] = mfma16(values4(pk[2 * q + i][d], k), qf[d], s[i]);
-                *reinterpret_cast<u32x4*>(tile + (16 * i + j) * kVStride + 32 * g + 8 * d) = values4(pv[2 * q + i][d], v);
-              }
-            }
+            for (int d = 0; d < 4; ++d)
+              *reinterpret_cast<u32x4*>(vtile + (16 * i + j) * kVStride + 32 * g + 8 * d) = values4(codes[d], f);
           }
-          then(q);
-          if (some) attend_scored<PARTS, CAREFUL>(tile, s, left - 32 * q, a.scale2, lane, st);
+          attend_scored<PARTS, CAREFUL>(vtile, s + 2 * q, left - 32 * q, a.scale2, lane, st);
         }
       }
     };
     enter(l, 0);
     w = l;
-    int2 where = make_int2(0, 0);
+    int32_t where = 0;
     if (l.s < ns) {
-      load_all(l, find(l));
+      load(l, find(l));
       load_q(0);
       step(w);
       if (w.s < ns) where = find(w);
     }
-    x = w;
-    step(x);
     while (l.s < ns) {
       const int32_t s = l.s;
       // first local row (from p0) that the column does not see
@@ -191,35 +179,37 @@ __device__ __forceinline__ void attend_streams(const AttendArgs& a, Lengths& n, 
           limit = visible_rows(a.kv_len[lo], a.q_off[lo + 1], y.t);
         }
       }
+      auto left_of = [&](const Cursor& u, int32_t rows) __attribute__((always_inline)) {
+        return u.tile < u.nctx ? rows : min(rows, limit - (u.tile - u.nctx) * kLocal);
+      };
       u32x4 qf[4];
 #pragma unroll
       for (int d = 0; d < 4; ++d) qf[d] = qn[d];
       State16 st;
       clear(st);
       while (l.s == s) {
-        // looked up before the next tile's loads: what is waited for first comes first
-        int2 after = where;
-        if (x.s < ns) after = find(x);
-        attend_tile(std::false_type(), l, limit, qf, st, [&](int q) __attribute__((always_inline)) {
-          if (w.s < ns) {
-            load(w, where, q);
-            if (q == 3 && w.s != s) load_q(w.s);
+        const int32_t rows = rows_of(l);
+        attend_tile(std::false_type(), l.tile < l.nctx, rows, left_of(l, rows), qf, st, [&]() __attribute__((always_inline)) {
+          l = w;
+          if (l.s < ns) {
+            load(l, where);
+            if (l.s != s) load_q(l.s);
+            step(w);
+            if (w.s < ns) where = find(w);
           }
         });
-        l = w;
-        w = x;
-        where = after;
-        step(x);
       }
       if (needs_care(st)) {
         clear(st);
         Cursor u = l;
         enter(u, s);
+#pragma unroll 1
         for (; u.tile < u.tile1; ++u.tile) {
-          load_all(u, find(u));
-          attend_tile(std::true_type(), u, limit, qf, st, [](int) {});
+          load(u, find(u));
+          const int32_t rows = rows_of(u);
+          attend_tile(std::true_type(), u.tile < u.nctx, rows, left_of(u, rows), qf, st, [] {});
         }
-        if (l.s < ns) load_all(l, find(l));       // the next piece's first tile again
+        if (l.s < ns) load(l, find(l));           // the next piece's first tile again
       }
       const Job job = seg[s].x;
       const Column y = column_of(a, job, layer, seg[s].set * kWaves + wave, j);

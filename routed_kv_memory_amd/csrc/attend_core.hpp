@@ -210,10 +210,9 @@ __device__ __forceinline__ Job job_of(const AttendArgs& a, const Lengths& n, int
   return x;
 }
 
-// How a cache holds its local rows: how many of them a streamed tile has (a memory row's bytes are a local row's only
-// in bf16; tiles take about as long either way).
+// How a cache holds its local rows: the rows of a streamed tile, memory rows (always bf16) and local ones.
 struct RowsBf16 {
-  static constexpr int kStreamLocal = kStreamRows;
+  static constexpr int kStreamCtx = kStreamRows, kStreamLocal = kStreamRows;
 };
 
 // Tiles: t memory rows each, then `local` local rows each; one for a job without rows (its columns are zero).
@@ -222,7 +221,7 @@ __device__ __forceinline__ int32_t tiles_of(const Job& x, int32_t t, int32_t loc
   return max(1, ctx_tiles(x, t) + (max(0, x.p1 - x.p0) + local - 1) / local);
 }
 template <class F>
-__device__ __forceinline__ int32_t stream_tiles(const Job& x) { return tiles_of(x, kStreamRows, F::kStreamLocal); }
+__device__ __forceinline__ int32_t stream_tiles(const Job& x) { return tiles_of(x, F::kStreamCtx, F::kStreamLocal); }
 __device__ __forceinline__ int32_t item_tiles(const Job& x) { return tiles_of(x, kTileRows, kTileRows); }
 
 // Keeps a uniform value in scalar registers: the compiler would rather load kernel arguments again in every
@@ -796,6 +795,26 @@ __device__ __forceinline__ void attend_scored(const uint16_t* tile, const f32x4*
   for (int d = 0; d < 8; ++d)
     add_values<PARTS, CAREFUL>(frag_of(lds_read_tr16(vsrc + 16 * d), lds_read_tr16(vsrc + 16 * kVStride + 16 * d)), pw,
                                st.o[d]);
+}
+
+// 16 rows whose scores are formed: the other half of the product's k axis holds nothing.
+template <int PARTS, bool CAREFUL>
+__device__ __forceinline__ void attend_scored16(const uint16_t* tile, f32x4 s, int32_t left, float scale2, int lane,
+                                                State16& st) {
+  const int j = lane & 15, g = lane >> 4;
+  float v[8], mt = -__builtin_huge_valf();
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    v[e] = e < 4 && 4 * g + (e & 3) < left ? s[e & 3] : -__builtin_huge_valf();
+    mt = fmaxf(mt, v[e]);
+  }
+  raise_to<CAREFUL>(rows4_max(mt), scale2, st);
+  u32x4 pw[PARTS];
+  weights<PARTS, CAREFUL>(v, scale2, st.neg, pw, st.l);
+  const uint16_t* vsrc = tile + (4 * g + (j >> 2)) * kVStride + 4 * (j & 3);
+#pragma unroll
+  for (int d = 0; d < 8; ++d)
+    add_values<PARTS, CAREFUL>(frag_of(lds_read_tr16(vsrc + 16 * d), make_uint2(0u, 0u)), pw, st.o[d]);
 }
 
 // 32 rows in the wave's tile: K rows while the scores are formed, then V rows; `then` once these are in.
