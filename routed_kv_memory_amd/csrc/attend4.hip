@@ -284,16 +284,26 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
   const int br = 16 * (wave & 1) + (lane >> 2), bb = lane & 3;
   // where its chunk d lies in a stage: chunk 4 bb + d permuted as the reads expect
   const int lds_row = (wave < 2 ? 0 : kTileRows * 16) + br * 16 + 4 * (bb ^ (wave < 2 ? (br >> 2) & 3 : br & 3));
-  auto fill_local = [&](int32_t t, u32x4* stage) __attribute__((always_inline)) {
-    const int32_t row = page_row(a, seq, p0 + min((t - nctx) * kTileRows + br, wg_most - 1));
-    const int32_t r = row & ((1 << shift) - 1);
-    const uint8_t* page = pages + (int64_t)(row >> shift) * (kRow4 << shift);
-    const u32x4 raw = *reinterpret_cast<const u32x4*>(page + codes4_at(head, r, shift) + 16 * bb);
-    const float s = scale4(page[scales4_at(head, r, shift) + bb]);
+  // The four local tiles from t on (the last again behind it): their rows, a step later their codes and scales.
+  auto find_local = [&](int32_t t, int32_t* rows) __attribute__((always_inline)) {
 #pragma unroll
-    for (int d = 0; d < 4; ++d) stage[lds_row + (d ^ (br & 3))] = values4(raw[d], s);
+    for (int i = 0; i < 4; ++i) rows[i] = page_row(a, seq, p0 + min((t + i - nctx) * kTileRows + br, wg_most - 1));
+  };
+  auto load_local = [&](const int32_t* rows, u32x4* raw, uint32_t* scale) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int32_t r = rows[i] & ((1 << shift) - 1);
+      const uint8_t* page = pages + (int64_t)(rows[i] >> shift) * (kRow4 << shift);
+      raw[i] = *reinterpret_cast<const u32x4*>(page + codes4_at(head, r, shift) + 16 * bb);
+      scale[i] = page[scales4_at(head, r, shift) + bb];
+    }
+  };
+  auto put_local = [&](u32x4 raw, uint32_t scale, u32x4* stage) __attribute__((always_inline)) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) stage[lds_row + (d ^ (br & 3))] = values4(raw[d], scale4(scale));
   };
   auto fill_ctx = [&](int32_t t, u32x4* stage) __attribute__((always_inline)) {
+    t = min(t, nctx - 1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = 8 * wave + 4 * i + (lane >> 4);
@@ -304,10 +314,6 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
                                        (lptr_t)(to + kTileRows * 16), 16, 0, 0);
     }
   };
-  auto fill = [&](int32_t t, u32x4* stage) __attribute__((always_inline)) {
-    if (t < nctx) fill_ctx(t, stage);
-    else fill_local(t, stage);
-  };
   const StageReads at(lane);
   State st;
   clear(st);
@@ -317,25 +323,51 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
   };
   const int32_t odd = jc & (kTileRows - 1) ? nctx - 1 : -1, whole_end = nctx + min(wg_most, least) / kTileRows;
   auto whole = [&](int32_t t) __attribute__((always_inline)) { return t != odd && t < whole_end; };
-  const int32_t last = tile1 - 1;
   auto pass = [&](auto care) __attribute__((always_inline)) {
     constexpr bool CAREFUL = decltype(care)::value;
     const uint32_t a0 = lds_at(stage0), a1 = lds_at(stage1), a2 = lds_at(stage2), a3 = lds_at(stage3);
-#pragma unroll 1
-    for (int32_t t = tile0; t < tile1; t += 4) {
-      fill(t, stage0);
-      fill(min(t + 1, last), stage1);
-      fill(min(t + 2, last), stage2);
-      fill(min(t + 3, last), stage3);
-      __builtin_amdgcn_s_waitcnt(0x70);           // vmcnt, lgkmcnt 0
-      __syncthreads();
+    auto use = [&](int32_t t, int32_t end) __attribute__((always_inline)) {
 #pragma unroll 1
       for (int i = turn; i < 4; i += share) {
-        if (t + i >= tile1) break;
+        if (t + i >= end) break;
         const u32x4* s = lds_ptr(i == 0 ? a0 : (i == 1 ? a1 : (i == 2 ? a2 : a3)));
         attend_tiles<PARTS, CAREFUL, 1>(nullptr, s, s, at, qf, t + i, whole(t + i), left_of, a.scale2, h, st);
       }
+      __builtin_amdgcn_s_waitcnt(0xC07F);         // what was read of the tiles is in registers
+      asm volatile("s_barrier" ::: "memory");
+    };
+    const int32_t ctx_end = min(tile1, nctx), local0 = max(tile0, nctx);
+    int32_t rows[4];
+    u32x4 raw[4];
+    uint32_t scale[4];
+    if (local0 < tile1) {
+      find_local(local0, rows);
+      load_local(rows, raw, scale);
+      find_local(local0 + 4, rows);
+    }
+#pragma unroll 1
+    for (int32_t t = tile0; t < ctx_end; t += 4) {
+      fill_ctx(t, stage0);
+      fill_ctx(t + 1, stage1);
+      fill_ctx(t + 2, stage2);
+      fill_ctx(t + 3, stage3);
+      __builtin_amdgcn_s_waitcnt(0x70);           // vmcnt, lgkmcnt 0
       __syncthreads();
+      use(t, ctx_end);
+    }
+#pragma unroll 1
+    for (int32_t t = local0; t < tile1; t += 4) {
+      put_local(raw[0], scale[0], stage0);
+      put_local(raw[1], scale[1], stage1);
+      put_local(raw[2], scale[2], stage2);
+      put_local(raw[3], scale[3], stage3);
+      if (t + 4 < tile1) {
+        load_local(rows, raw, scale);
+        find_local(t + 8, rows);
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);         // lgkmcnt 0: the tiles are written; the next ones stay on their way
+      asm volatile("s_barrier" ::: "memory");
+      use(t, tile1);
     }
   };
   pass(std::false_type());
