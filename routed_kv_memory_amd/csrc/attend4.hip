@@ -233,10 +233,10 @@ template <bool BF16_OUT>
 __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& n, ItemShared& z, u32x4* stage0, u32x4* stage1,
                                             u32x4* stage2, u32x4* stage3, int64_t layer, int tid) {
   constexpr int PARTS = BF16_OUT ? 1 : 3;
-  const int lane = tid & 63, wave = tid >> 6;
+  auto uni = [](int32_t v) { return __builtin_amdgcn_readfirstlane(v); };
+  const int lane = tid & 63, wave = uni(tid >> 6);
   const int c = lane & 31, h = lane >> 5;
   const Item& it = z.item;
-  auto uni = [](int32_t v) { return __builtin_amdgcn_readfirstlane(v); };
   const Job x = it.x;
   // fewer column blocks than waves: `share` waves take a block's columns and the tiles in turn
   const int32_t blocks = uni(it.blocks), unit = uni(it.unit), share = kWaves / blocks;
@@ -265,14 +265,21 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
   }
   if (it.first && turn == 0 && y.live && h == 0 && (c & (a.G - 1)) == 0)
     describe(a, x, y, layer, it.parts, it.unit < 0 ? 0 : kBlockUnits * cb, it.width, it.width * kHeads, c);
-  if (lane == 0) z.most[wave] = most;
+  if (lane == 0) {
+    z.most[wave] = most;
+    z.least[wave] = least;
+  }
   __syncthreads();                                   // the lengths' memory becomes the tiles'
 
   const int32_t jc = uni(x.c), p0 = uni(x.p0), seq = uni(x.seq), nctx = (jc + kTileRows - 1) / kTileRows;
-  int32_t wg_most = 0;
+  int32_t wg_most = 0, wg_least = 0x7FFFFFFF;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) wg_most = max(wg_most, z.most[w]);
+  for (int w = 0; w < kWaves; ++w) {
+    wg_most = max(wg_most, z.most[w]);
+    wg_least = min(wg_least, z.least[w]);
+  }
   wg_most = uni(wg_most);
+  wg_least = uni(wg_least);
   tile1 = min(tile1, nctx + (wg_most + kTileRows - 1) / kTileRows);
 
   const int64_t ctx_at = (layer * a.n_groups + uni(x.grp)) * (int64_t)a.max_ctx * kRow + head * kDim;
@@ -284,23 +291,27 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
   const int br = 16 * (wave & 1) + (lane >> 2), bb = lane & 3;
   // where its chunk d lies in a stage: chunk 4 bb + d permuted as the reads expect
   const int lds_row = (wave < 2 ? 0 : kTileRows * 16) + br * 16 + 4 * (bb ^ (wave < 2 ? (br >> 2) & 3 : br & 3));
-  // The four local tiles from t on (the last again behind it): their rows, a step later their codes and scales.
-  auto find_local = [&](int32_t t, int32_t* rows) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) rows[i] = page_row(a, seq, p0 + min((t + i - nctx) * kTileRows + br, wg_most - 1));
+  // The four local tiles from t on (the last row again behind it): their pages, a step later their codes and scales.
+  auto local_of = [&](int32_t t, int i) __attribute__((always_inline)) {
+    return p0 + min((t + i - nctx) * kTileRows + br, wg_most - 1);
   };
-  auto load_local = [&](const int32_t* rows, u32x4* raw, uint32_t* scale) __attribute__((always_inline)) {
+  auto find_local = [&](int32_t t, int32_t* page) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) page[i] = a.page_table[(int64_t)seq * a.max_pages + (local_of(t, i) >> shift)];
+  };
+  auto load_local = [&](int32_t t, const int32_t* page, u32x4* raw, uint32_t* scales) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int32_t r = rows[i] & ((1 << shift) - 1);
-      const uint8_t* page = pages + (int64_t)(rows[i] >> shift) * (kRow4 << shift);
-      raw[i] = *reinterpret_cast<const u32x4*>(page + codes4_at(head, r, shift) + 16 * bb);
-      scale[i] = page[scales4_at(head, r, shift) + bb];
+      const int32_t r = local_of(t, i) & ((1 << shift) - 1);
+      const uint8_t* p = pages + (int64_t)clampi(page[i], 0, a.n_pages - 1) * (kRow4 << shift);
+      raw[i] = *reinterpret_cast<const u32x4*>(p + codes4_at(head, r, shift) + 16 * bb);
+      scales[i] = *reinterpret_cast<const uint32_t*>(p + scales4_at(head, r, shift));      // of the row's four blocks
     }
   };
-  auto put_local = [&](u32x4 raw, uint32_t scale, u32x4* stage) __attribute__((always_inline)) {
+  auto put_local = [&](u32x4 raw, uint32_t scales, u32x4* stage) __attribute__((always_inline)) {
+    const float f = scale4(scales >> (8 * bb) & 255u);
 #pragma unroll
-    for (int d = 0; d < 4; ++d) stage[lds_row + (d ^ (br & 3))] = values4(raw[d], scale4(scale));
+    for (int d = 0; d < 4; ++d) stage[lds_row + (d ^ (br & 3))] = values4(raw[d], f);
   };
   auto fill_ctx = [&](int32_t t, u32x4* stage) __attribute__((always_inline)) {
     t = min(t, nctx - 1);
@@ -314,7 +325,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
                                        (lptr_t)(to + kTileRows * 16), 16, 0, 0);
     }
   };
-  const StageReads at(lane);
+  StageReads at(lane);
   State st;
   clear(st);
   // rows of tile t that a column sees, or more; whether all the wave's columns see all of it
@@ -323,9 +334,161 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
   };
   const int32_t odd = jc & (kTileRows - 1) ? nctx - 1 : -1, whole_end = nctx + min(wg_most, least) / kTileRows;
   auto whole = [&](int32_t t) __attribute__((always_inline)) { return t != odd && t < whole_end; };
+  const uint32_t a0 = lds_at(stage0), a1 = lds_at(stage1), a2 = lds_at(stage2), a3 = lds_at(stage3);
+  // Whole local tiles, a unit of two a step, whose 16 rows a wave lie in one page.  S = 1: a wave takes both tiles;
+  // S = 2: two waves share a column block and take one each.  A wave forms the scores of its next tile while this
+  // one's turn into weights: matrix and vector work of one wave that do not wait for each other.  So K is ahead of V
+  // by a tile (S = 1) or a unit (S = 2), and LDS holds K and V of four tiles, two that are read and two that are
+  // written.  Codes are on their way for a step before they are turned into bf16.
+  auto units = [&](auto per, int32_t first, int32_t n) __attribute__((always_inline)) {
+    constexpr int S = decltype(per)::value;
+    constexpr int kAhead = S;                     // tiles that K is ahead by
+    // scalar loads, and row addresses in scalar registers
+    const auto* table = (const __attribute__((address_space(4))) int32_t*)kept(a.page_table + (int64_t)seq * a.max_pages);
+    typedef const __attribute__((address_space(1))) uint8_t* pool_t;
+    const pool_t all_k = (pool_t)kept((const uint8_t*)a.k_pages + layer_at), all_v = (pool_t)kept((const uint8_t*)a.v_pages + layer_at);
+    const int32_t last_page = kept(a.n_pages - 1), page_bytes = kept(kRow4 << shift);
+    const int32_t head_codes = kept(codes4_at(head, 0, shift)), head_scales = kept(scales4_at(head, 0, shift));
+    const int32_t row_w = uni(p0 + (first - nctx) * kTileRows + 16 * wave);
+    const int32_t last_row = uni(p0 + (first - nctx + 2 * n - 1) * kTileRows + 16 * (wave & 1));
+    // first of this wave's 16 rows of tiles t and t + 1 (t from `first` on; the last tile again behind it)
+    auto row_of = [&](int32_t t) __attribute__((always_inline)) { return min(row_w + t * kTileRows, last_row); };
+    auto find = [&](int32_t t) __attribute__((always_inline)) -> int32_t { return table[row_of(t) >> shift]; };
+    struct Raw {
+      u32x4 codes;
+      uint32_t scales;       // of the row's four blocks (a byte's extension would be waited for long before its use)
+    };
+    auto load = [&](pool_t pool, int32_t t, int32_t page) __attribute__((always_inline)) -> Raw {
+      const int32_t r = row_of(t) & ((1 << shift) - 1);
+      const pool_t p = pool + (int64_t)clampi(page, 0, last_page) * page_bytes;
+      const pool_t codes = p + (head_codes + r * kCodes4), scales = p + (head_scales + r * kBlocks4);
+      Raw x;
+      x.codes = *(const __attribute__((address_space(1))) u32x4*)(codes + (uint32_t)(16 * lane));
+      x.scales = *(const __attribute__((address_space(1))) uint32_t*)(scales + (uint32_t)(4 * (lane >> 2)));
+      return x;
+    };
+    // a tile's place: K in stages 0 and 1, V in 2 and 3, of four tiles in turn
+    auto slot = [&](int32_t t) __attribute__((always_inline)) { return (uint32_t)(8192 * (t & 3)); };
+    const int part = br * 16, at_k = part + 4 * (bb ^ ((br >> 2) & 3)), at_v = part + 4 * (bb ^ (br & 3));
+    const uint32_t to_k = 16 * (at_k + (br & 3)), to_v = 16 * (at_v + (br & 3));
+    auto put = [&](uint32_t base, uint32_t to, const Raw& x) __attribute__((always_inline)) {
+      const float f = scale4(x.scales >> (8 * bb) & 255u);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) *const_cast<u32x4*>(lds_ptr((to ^ (16 * d)) + base)) = values4(x.codes[d], f);
+    };
+    // waves 0 and 1 bring the first tile of two, 2 and 3 the second
+    const int32_t second = wave >> 1;
+    // K of the tiles before those that steps bring, V of unit 0
+    if (S == 1) {
+      const Raw k0 = load(all_k, 0, find(0)), k1 = load(all_k, 1, find(1)), v0 = load(all_v, 0, find(0));
+      if (second == 0) put(a0 + slot(0), to_k, k0);
+      put(a0 + (second ? slot(2) : slot(1)), to_k, k1);
+      put(a2 + (second ? slot(1) : slot(0)), to_v, v0);
+    } else {
+      const Raw k0 = load(all_k, 0, find(0)), k1 = load(all_k, 2, find(2)), v0 = load(all_v, 0, find(0));
+      put(a0 + (second ? slot(1) : slot(0)), to_k, k0);
+      put(a0 + (second ? slot(3) : slot(2)), to_k, k1);
+      put(a2 + (second ? slot(1) : slot(0)), to_v, v0);
+    }
+    // step u brings K of tiles 2 u + 2 + kAhead and the next, V of 2 u + 2 and the next
+    Raw rk = load(all_k, 2 + kAhead, find(2 + kAhead)), rv = load(all_v, 2, find(2));
+    int32_t page_k = find(4 + kAhead), page_v = find(4);
+    auto shift_reads = [&](int by) __attribute__((always_inline)) {    // to this wave's tile of a unit
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        at.kb[d] += by;
+        asm("" : "+v"(at.kb[d]));                 // else the old ones are kept beside
+      }
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        at.vb[d] += by;
+        asm("" : "+v"(at.vb[d]));
+      }
+    };
+    if (S == 2) shift_reads(8192 * turn);
+    auto form = [&](uint32_t at_slot) __attribute__((always_inline)) {
+      f32x16 s = zeros16();
+#pragma unroll
+      for (int d = 0; d < 8; ++d) s = mfma32(at.k(lds_ptr(a0 + at_slot), d), qf[d], s);
+      return s;
+    };
+    __builtin_amdgcn_s_waitcnt(0xC07F);           // lgkmcnt 0
+    asm volatile("s_barrier" ::: "memory");
+    f32x16 s = form(0);
+    float top = halves_max(max16(s));
+    // the tile whose scores are formed: its V at v_slot; the next one's K at k_slot
+    auto tile = [&](uint32_t k_slot, uint32_t v_slot) __attribute__((always_inline)) {
+      u32x4 kf[8], vf[2][4];
+#pragma unroll
+      for (int d = 0; d < 8; ++d) kf[d] = at.k(lds_ptr(a0 + k_slot), d);
+      __builtin_amdgcn_sched_barrier(0);
+      raise_to<false>(top, a.scale2, st);
+      auto read_v = [&](int m) __attribute__((always_inline)) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int d = 0; d < 4; ++d)      // V rows lie behind a stage's 32 K rows for `v`, 8 KB
+          vf[m][d] = at.v(lds_ptr(a2 + v_slot - 8192), m, d);
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      u32x4 pw[2][PARTS];
+      auto weigh = [&](int m) __attribute__((always_inline)) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = s[8 * m + e];
+        weights<PARTS, false>(v, a.scale2, st.neg, pw[m], st.l);
+      };
+      auto sum = [&](int m) __attribute__((always_inline)) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) add_values<PARTS, false>(vf[m][d], pw[m], st.o[d]);
+      };
+      read_v(0);
+      f32x16 t = zeros16();
+#pragma unroll
+      for (int d = 0; d < 8; ++d) t = mfma32(kf[d], qf[d], t);
+      weigh(0);
+      weigh(1);
+      s = t;
+      read_v(1);
+      sum(0);
+      sum(1);
+      top = halves_max(max16(s));
+    };
+    // u even: i = 0
+    auto step = [&](auto odd_u, int32_t u) __attribute__((always_inline)) {
+      constexpr int i = decltype(odd_u)::value, T = 2 * i;       // its first tile, of four
+      __builtin_amdgcn_s_waitcnt(0xC07F);         // this wave's part of the next tiles is written
+      asm volatile("s_barrier" ::: "memory");
+      const uint32_t k_to = a0 + 8192 * ((T + 2 + kAhead) & 3), k_to2 = a0 + 8192 * ((T + 3 + kAhead) & 3);
+      const uint32_t v_to = a2 + 8192 * ((T + 2) & 3);
+      auto bring = [&]() __attribute__((always_inline)) {
+        put(second ? k_to2 : k_to, to_k, rk);
+        put(second ? v_to + 8192 : v_to, to_v, rv);
+        rk = load(all_k, 2 * u + 4 + kAhead, page_k);
+        rv = load(all_v, 2 * u + 4, page_v);
+        page_k = find(2 * u + 6 + kAhead);
+        page_v = find(2 * u + 6);
+      };
+      if (S == 1) {
+        tile(8192 * ((T + 1) & 3), 8192 * T);
+        bring();
+        tile(8192 * ((T + 2) & 3), 8192 * (T + 1));
+      } else {
+        tile(8192 * ((T + 2) & 3), 8192 * T);
+        bring();
+      }
+    };
+#pragma unroll 1
+    for (int32_t u = 0; u + 1 < n; u += 2) {      // pairs: each step's loads are always followed by the other's
+      step(std::integral_constant<int, 0>(), u);
+      step(std::integral_constant<int, 1>(), u + 1);
+    }
+    if (n & 1) step(std::integral_constant<int, 0>(), n - 1);
+    if (S == 2) shift_reads(-8192 * turn);
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("s_barrier" ::: "memory");
+  };
   auto pass = [&](auto care) __attribute__((always_inline)) {
     constexpr bool CAREFUL = decltype(care)::value;
-    const uint32_t a0 = lds_at(stage0), a1 = lds_at(stage1), a2 = lds_at(stage2), a3 = lds_at(stage3);
     auto use = [&](int32_t t, int32_t end) __attribute__((always_inline)) {
 #pragma unroll 1
       for (int i = turn; i < 4; i += share) {
@@ -336,15 +499,8 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
       __builtin_amdgcn_s_waitcnt(0xC07F);         // what was read of the tiles is in registers
       asm volatile("s_barrier" ::: "memory");
     };
-    const int32_t ctx_end = min(tile1, nctx), local0 = max(tile0, nctx);
-    int32_t rows[4];
-    u32x4 raw[4];
-    uint32_t scale[4];
-    if (local0 < tile1) {
-      find_local(local0, rows);
-      load_local(rows, raw, scale);
-      find_local(local0 + 4, rows);
-    }
+    const int32_t ctx_end = min(tile1, nctx);
+    int32_t local0 = max(tile0, nctx);
 #pragma unroll 1
     for (int32_t t = tile0; t < ctx_end; t += 4) {
       fill_ctx(t, stage0);
@@ -355,15 +511,30 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
       __syncthreads();
       use(t, ctx_end);
     }
+    if (!CAREFUL && blocks == kWaves && shift >= 4 && (p0 & 15) == 0) {
+      const int32_t tiles = min(tile1, nctx + min(wg_most, wg_least) / kTileRows) - local0, n = tiles / 2;
+      if (n > 0) {
+        units(std::integral_constant<int, 1>(), local0, n);
+        local0 += 2 * n;
+      }
+    }
+    int32_t page[4];
+    u32x4 raw[4];
+    uint32_t scales[4];
+    if (local0 < tile1) {
+      find_local(local0, page);
+      load_local(local0, page, raw, scales);
+      find_local(local0 + 4, page);
+    }
 #pragma unroll 1
     for (int32_t t = local0; t < tile1; t += 4) {
-      put_local(raw[0], scale[0], stage0);
-      put_local(raw[1], scale[1], stage1);
-      put_local(raw[2], scale[2], stage2);
-      put_local(raw[3], scale[3], stage3);
+      put_local(raw[0], scales[0], stage0);
+      put_local(raw[1], scales[1], stage1);
+      put_local(raw[2], scales[2], stage2);
+      put_local(raw[3], scales[3], stage3);
       if (t + 4 < tile1) {
-        load_local(rows, raw, scale);
-        find_local(t + 8, rows);
+        load_local(t + 4, page, raw, scales);
+        find_local(t + 8, page);
       }
       __builtin_amdgcn_s_waitcnt(0xC07F);         // lgkmcnt 0: the tiles are written; the next ones stay on their way
       asm volatile("s_barrier" ::: "memory");
@@ -381,7 +552,8 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
 template <bool BF16_OUT>
 __global__ void __launch_bounds__(kThreads, 2)
 attend4_kernel(const AttendArgs a) {
-  __shared__ u32x4 stage0[kStage], stage1[kStage], stage2[kStage], stage3[kStage];
+  __shared__ u32x4 stages[4 * kStage];
+  u32x4 *const stage0 = stages, *const stage1 = stages + kStage, *const stage2 = stages + 2 * kStage, *const stage3 = stages + 3 * kStage;
   __shared__ union {
     ItemShared item;
     struct {

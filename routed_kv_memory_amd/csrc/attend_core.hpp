@@ -935,6 +935,7 @@ __device__ __forceinline__ void attend_tiles(const u32x4* kf, const u32x4* stage
 struct ItemShared {
   Item item;
   int32_t most[kWaves];                   // local rows that a wave's columns see
+  int32_t least[kWaves];                  // and that all of them see
   float m[kWaves][kCols], l[kWaves][kCols];
 };
 
