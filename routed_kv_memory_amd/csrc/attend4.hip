@@ -335,16 +335,15 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
   const int32_t odd = jc & (kTileRows - 1) ? nctx - 1 : -1, whole_end = nctx + min(wg_most, least) / kTileRows;
   auto whole = [&](int32_t t) __attribute__((always_inline)) { return t != odd && t < whole_end; };
   const uint32_t a0 = lds_at(stage0), a1 = lds_at(stage1), a2 = lds_at(stage2), a3 = lds_at(stage3);
-  // Whole local tiles, a unit of two a step, whose 16 rows a wave lie in one page.  S = 1: a wave takes both tiles;
-  // S = 2: two waves share a column block and take one each.  A wave forms the scores of its next tile while this
-  // one's turn into weights: matrix and vector work of one wave that do not wait for each other.  So K is ahead of V
-  // by a tile (S = 1) or a unit (S = 2), and LDS holds K and V of four tiles, two that are read and two that are
+  // Four column blocks: whole local tiles, two a step, whose 16 rows a wave lie in one page.  A wave forms the scores of
+  // its next tile while this one's turn into weights: matrix and vector work of one wave that do not wait for each
+  // other.  So K is a tile ahead of V, and LDS holds K and V of four tiles, two that are read and two that are
   // written.  Codes are on their way for a step before they are turned into bf16.
-  auto units = [&](auto per, int32_t first, int32_t n) __attribute__((always_inline)) {
-    constexpr int S = decltype(per)::value;
-    constexpr int kAhead = S;                     // tiles that K is ahead by
-    // scalar loads, and row addresses in scalar registers
-    const auto* table = (const __attribute__((address_space(4))) int32_t*)kept(a.page_table + (int64_t)seq * a.max_pages);
+  auto units = [&](int32_t first, int32_t n) __attribute__((always_inline)) {
+    // Pages by vector loads, of one address: a scalar load on its way would make every wait for LDS a wait for all of it.
+    // Row addresses are in scalar registers.
+    const int32_t* table = kept(a.page_table + (int64_t)seq * a.max_pages);
+    const int zero = threadIdx.x >> 8;            // 0, but not to the compiler
     typedef const __attribute__((address_space(1))) uint8_t* pool_t;
     const pool_t all_k = (pool_t)kept((const uint8_t*)a.k_pages + layer_at), all_v = (pool_t)kept((const uint8_t*)a.v_pages + layer_at);
     const int32_t last_page = kept(a.n_pages - 1), page_bytes = kept(kRow4 << shift);
@@ -353,14 +352,14 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
     const int32_t last_row = uni(p0 + (first - nctx + 2 * n - 1) * kTileRows + 16 * (wave & 1));
     // first of this wave's 16 rows of tiles t and t + 1 (t from `first` on; the last tile again behind it)
     auto row_of = [&](int32_t t) __attribute__((always_inline)) { return min(row_w + t * kTileRows, last_row); };
-    auto find = [&](int32_t t) __attribute__((always_inline)) -> int32_t { return table[row_of(t) >> shift]; };
+    auto find = [&](int32_t t) __attribute__((always_inline)) -> int32_t { return table[(row_of(t) >> shift) + zero]; };
     struct Raw {
       u32x4 codes;
       uint32_t scales;       // of the row's four blocks (a byte's extension would be waited for long before its use)
     };
     auto load = [&](pool_t pool, int32_t t, int32_t page) __attribute__((always_inline)) -> Raw {
       const int32_t r = row_of(t) & ((1 << shift) - 1);
-      const pool_t p = pool + (int64_t)clampi(page, 0, last_page) * page_bytes;
+      const pool_t p = pool + (int64_t)clampi(uni(page), 0, last_page) * page_bytes;
       const pool_t codes = p + (head_codes + r * kCodes4), scales = p + (head_scales + r * kBlocks4);
       Raw x;
       x.codes = *(const __attribute__((address_space(1))) u32x4*)(codes + (uint32_t)(16 * lane));
@@ -378,34 +377,16 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
     };
     // waves 0 and 1 bring the first tile of two, 2 and 3 the second
     const int32_t second = wave >> 1;
-    // K of the tiles before those that steps bring, V of unit 0
-    if (S == 1) {
+    // K of tiles 0 to 2, V of 0 and 1
+    {
       const Raw k0 = load(all_k, 0, find(0)), k1 = load(all_k, 1, find(1)), v0 = load(all_v, 0, find(0));
       if (second == 0) put(a0 + slot(0), to_k, k0);
       put(a0 + (second ? slot(2) : slot(1)), to_k, k1);
       put(a2 + (second ? slot(1) : slot(0)), to_v, v0);
-    } else {
-      const Raw k0 = load(all_k, 0, find(0)), k1 = load(all_k, 2, find(2)), v0 = load(all_v, 0, find(0));
-      put(a0 + (second ? slot(1) : slot(0)), to_k, k0);
-      put(a0 + (second ? slot(3) : slot(2)), to_k, k1);
-      put(a2 + (second ? slot(1) : slot(0)), to_v, v0);
     }
-    // step u brings K of tiles 2 u + 2 + kAhead and the next, V of 2 u + 2 and the next
-    Raw rk = load(all_k, 2 + kAhead, find(2 + kAhead)), rv = load(all_v, 2, find(2));
-    int32_t page_k = find(4 + kAhead), page_v = find(4);
-    auto shift_reads = [&](int by) __attribute__((always_inline)) {    // to this wave's tile of a unit
-#pragma unroll
-      for (int d = 0; d < 8; ++d) {
-        at.kb[d] += by;
-        asm("" : "+v"(at.kb[d]));                 // else the old ones are kept beside
-      }
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        at.vb[d] += by;
-        asm("" : "+v"(at.vb[d]));
-      }
-    };
-    if (S == 2) shift_reads(8192 * turn);
+    // step u brings K of tiles 2 u + 3 and the next, V of 2 u + 2 and the next
+    Raw rk = load(all_k, 3, find(3)), rv = load(all_v, 2, find(2));
+    int32_t page_k = find(5), page_v = find(4);
     auto form = [&](uint32_t at_slot) __attribute__((always_inline)) {
       f32x16 s = zeros16();
 #pragma unroll
@@ -458,24 +439,14 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
       constexpr int i = decltype(odd_u)::value, T = 2 * i;       // its first tile, of four
       __builtin_amdgcn_s_waitcnt(0xC07F);         // this wave's part of the next tiles is written
       asm volatile("s_barrier" ::: "memory");
-      const uint32_t k_to = a0 + 8192 * ((T + 2 + kAhead) & 3), k_to2 = a0 + 8192 * ((T + 3 + kAhead) & 3);
-      const uint32_t v_to = a2 + 8192 * ((T + 2) & 3);
-      auto bring = [&]() __attribute__((always_inline)) {
-        put(second ? k_to2 : k_to, to_k, rk);
-        put(second ? v_to + 8192 : v_to, to_v, rv);
-        rk = load(all_k, 2 * u + 4 + kAhead, page_k);
-        rv = load(all_v, 2 * u + 4, page_v);
-        page_k = find(2 * u + 6 + kAhead);
-        page_v = find(2 * u + 6);
-      };
-      if (S == 1) {
-        tile(8192 * ((T + 1) & 3), 8192 * T);
-        bring();
-        tile(8192 * ((T + 2) & 3), 8192 * (T + 1));
-      } else {
-        tile(8192 * ((T + 2) & 3), 8192 * T);
-        bring();
-      }
+      tile(8192 * (T + 1), 8192 * T);
+      put(a0 + 8192 * (second ? T : (T + 3) & 3), to_k, rk);
+      put(a2 + 8192 * (second ? (T + 3) & 3 : (T + 2) & 3), to_v, rv);
+      rk = load(all_k, 2 * u + 5, page_k);
+      rv = load(all_v, 2 * u + 4, page_v);
+      page_k = find(2 * u + 7);
+      page_v = find(2 * u + 6);
+      tile(8192 * ((T + 2) & 3), 8192 * (T + 1));
     };
 #pragma unroll 1
     for (int32_t u = 0; u + 1 < n; u += 2) {      // pairs: each step's loads are always followed by the other's
@@ -483,7 +454,6 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
       step(std::integral_constant<int, 1>(), u + 1);
     }
     if (n & 1) step(std::integral_constant<int, 0>(), n - 1);
-    if (S == 2) shift_reads(-8192 * turn);
     __builtin_amdgcn_s_waitcnt(0xC07F);
     asm volatile("s_barrier" ::: "memory");
   };
@@ -514,7 +484,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Lengths& 
     if (!CAREFUL && blocks == kWaves && shift >= 4 && (p0 & 15) == 0) {
       const int32_t tiles = min(tile1, nctx + min(wg_most, wg_least) / kTileRows) - local0, n = tiles / 2;
       if (n > 0) {
-        units(std::integral_constant<int, 1>(), local0, n);
+        units(local0, n);
         local0 += 2 * n;
       }
     }
