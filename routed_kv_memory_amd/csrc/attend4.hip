@@ -69,16 +69,23 @@ __device__ __forceinline__ void attend_streams(const AttendArgs& a, Lengths& n, 
     auto step = [&](Cursor& u) __attribute__((always_inline)) {
       if (++u.tile >= u.tile1) enter(u, u.s + 1);
     };
-    auto find = [&](const Cursor& u) __attribute__((always_inline)) -> int32_t {
+    // The tile's row for lane r (copies of the last behind it), and its page as it stands in the table: nothing is done
+    // with that before its rows are loaded, else it would be waited for, and all loads before it.
+    auto row_of = [&](const Cursor& u) __attribute__((always_inline)) -> int32_t {
       if (u.tile < u.nctx) return min(u.tile * kCtx + j, u.c - 1);
-      return u.p1 > u.p0 ? page_row(a, u.seq, min(u.p0 + (u.tile - u.nctx) * kLocal + lane, u.p1 - 1)) : 0;
+      return max(0, min(u.p0 + (u.tile - u.nctx) * kLocal + lane, u.p1 - 1));
+    };
+    auto find = [&](const Cursor& u) __attribute__((always_inline)) -> int32_t {
+      return u.tile < u.nctx ? 0 : a.page_table[(int64_t)u.seq * a.max_pages + (row_of(u) >> shift)];
     };
     // Memory tile: pk[i], pv[i] hold row 4 i + g, dims 8 j ...  Local tile: codes of row 16 i + j, dims 32 g ..,
-    // and sk[i], sv[i] their scales (of a memory tile: nothing, but loaded all the same).
+    // and sk[i], sv[i] the scales of its four blocks (of a memory tile: nothing, but loaded all the same).
     u32x4 pk[4], pv[4];
     uint32_t sk[4], sv[4];
     auto load = [&](const Cursor& u, int32_t where) __attribute__((always_inline)) {
-      const bool ctx = u.tile < u.nctx;           // uniform, as all but `row`
+      const bool ctx = u.tile < u.nctx;           // uniform, as all but `rows` and `row`
+      const int32_t lr = row_of(u);
+      const int32_t rows = ctx ? lr : (clampi(where, 0, a.n_pages - 1) << shift) + (lr & ((1 << shift) - 1));
       const char *kb = ctx ? ctx_k : page_k, *vb = ctx ? ctx_v : page_v;
       const int64_t base = ctx ? 2 * ((ctx_row + u.grp * (int64_t)max_ctx) * kRow + u.head * kDim) : (int64_t)(u.head * kCodes4 << shift);
       const int64_t scales = ctx ? base : (int64_t)(kHeads * kCodes4 << shift) + (u.head * kBlocks4 << shift);
@@ -86,13 +93,13 @@ __device__ __forceinline__ void attend_streams(const AttendArgs& a, Lengths& n, 
       const int step_s = ctx ? 2 * kRow : kBlocks4, first = ctx ? g : j, each = ctx ? 4 : 16, at = 16 * (ctx ? j : g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int32_t row = __shfl(where, each * i + first, 64);
+        const int32_t row = __shfl(rows, each * i + first, 64);
         const int64_t page = (int64_t)(row >> by) * step_hi;
         const int64_t r = (int64_t)(row & (int32_t)((1u << by) - 1u));
         pk[i] = *reinterpret_cast<const u32x4*>(kb + base + page + r * step_lo + at);
         pv[i] = *reinterpret_cast<const u32x4*>(vb + base + page + r * step_lo + at);
-        sk[i] = *reinterpret_cast<const uint8_t*>(kb + scales + page + r * step_s + g);
-        sv[i] = *reinterpret_cast<const uint8_t*>(vb + scales + page + r * step_s + g);
+        sk[i] = *reinterpret_cast<const uint32_t*>(kb + scales + page + r * step_s);
+        sv[i] = *reinterpret_cast<const uint32_t*>(vb + scales + page + r * step_s);
       }
     };
     // rows of the cursor's tile, or more (0: none)
@@ -127,11 +134,12 @@ __device__ __forceinline__ void attend_streams(const AttendArgs& a, Lengths& n, 
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+          const float f = scale4(sk[i] >> (8 * g) & 255u);
           s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int d = 0; d < 4; ++d) s[i] = mfma16(values4(pk[i][d], scale4(sk[i])), qf[d], s[i]);
+          for (int d = 0; d < 4; ++d) s[i] = mfma16(values4(pk[i][d], f), qf[d], s[i]);
           raw[64 * i + lane] = pv[i];
-          sp |= sv[i] << (8 * i);
+          sp |= (sv[i] >> (8 * g) & 255u) << (8 * i);
         }
       }
       then();
