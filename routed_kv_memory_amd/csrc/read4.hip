@@ -3,14 +3,18 @@
 // Packed row t (i-th of sequence b's) is local row row0[b] + i of b: row r % P of page page_table[b][r / P], each
 // code as the bf16 value it stands for (cache4.hpp).
 //
-// One wave takes one row in one layer: 8 lanes a head, 16 dims each.
+// Bound: HBM, nearly all of it what is written (5,184 bytes a row and layer, 4,096 of them out): 540,000 rows take 528 us
+// (5.3 TB/s), a few rows 8 us.  One wave takes one row in one layer; lane l holds dims 8 l .. and 512 + 8 l .. of its
+// 8 x 128, so each store of the wave is 1 KiB without gaps (16 dims a lane, two stores of every other 16 bytes: 609 us where
+// this takes 415, ragged conversations).  Several rows a wave, looked up at once, are slower: 555 us with two, 604 with four; 333 rows in 18
+// layers 8.2 us with one, 9.3 with four.
 #include "cache4.hpp"
 #include "msa_kernels.hpp"
 
 namespace msa {
 namespace {
 
-constexpr int kReadWaves = 4;              // rows per workgroup
+constexpr int kReadWaves = 4;              // rows of a workgroup
 
 __global__ void __launch_bounds__(64 * kReadWaves)
 read4_kernel(int32_t B, int32_t n_rows, const int32_t* __restrict__ row_off, const int32_t* __restrict__ row0,
@@ -18,10 +22,10 @@ read4_kernel(int32_t B, int32_t n_rows, const int32_t* __restrict__ row_off, con
              const uint8_t* __restrict__ k_pages, const uint8_t* __restrict__ v_pages, uint16_t* __restrict__ k_out,
              uint16_t* __restrict__ v_out) {
   const int lane = threadIdx.x & 63;
-  const int32_t t = blockIdx.x * kReadWaves + (threadIdx.x >> 6);
+  const int32_t t = __builtin_amdgcn_readfirstlane(blockIdx.x * kReadWaves + (threadIdx.x >> 6));
   const int64_t layer = blockIdx.y;
   if (t >= n_rows) return;                  // whole waves; no barrier below
-  const int32_t b = seq_of_token(row_off, B, t, lane);
+  const int32_t b = __builtin_amdgcn_readfirstlane(seq_of_token(row_off, B, t, lane));
   if (b >= B) return;                       // rows behind the last sequence are left as they are
   const int32_t q0 = row_off[b];
   if (t < q0 || t >= row_off[b + 1]) return;          // offsets that are not ascending
@@ -29,24 +33,27 @@ read4_kernel(int32_t B, int32_t n_rows, const int32_t* __restrict__ row_off, con
   int32_t page = -1;
   if (row >= 0 && (row >> page_shift) < max_pages) page = page_table[(int64_t)b * max_pages + (row >> page_shift)];
   const bool have = page >= 0 && page < n_pages;
-  const int64_t from = ((layer * n_pages + (have ? page : 0)) << page_shift) * kRow4;
-  const int head = lane >> 3, j = lane & 7, r = (int)(row & ((1 << page_shift) - 1));
-  const int64_t at = (layer * n_rows + t) * kRow + head * kDim + 16 * j;
-  const int64_t codes = from + codes4_at(head, r, page_shift) + 8 * j;
-  const int64_t scale = from + scales4_at(head, r, page_shift) + (j >> 1);
-  auto put = [&](const uint8_t* pages, uint16_t* out) {
-    u32x4 lo = {0u, 0u, 0u, 0u}, hi = lo;   // no such row
-    if (have) {
-      const uint2 w = *reinterpret_cast<const uint2*>(pages + codes);
-      const float s = scale4(pages[scale]);
-      lo = values4(w.x, s);
-      hi = values4(w.y, s);
+  const int64_t from = ((layer * n_pages + page) << page_shift) * kRow4;
+  const int r = (int)(row & ((1 << page_shift) - 1));
+  const int d = lane & 15;                  // dims 8 d .. of heads lane >> 4 and 4 + (lane >> 4)
+  uint32_t codes[4] = {0u, 0u, 0u, 0u}, scales[4] = {0u, 0u, 0u, 0u};      // zeros: no such row
+  if (have) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int head = 4 * h + (lane >> 4);
+      const int64_t c = from + codes4_at(head, r, page_shift) + 4 * d, s = from + scales4_at(head, r, page_shift) + (d >> 2);
+      codes[h] = *reinterpret_cast<const uint32_t*>(k_pages + c);
+      codes[2 + h] = *reinterpret_cast<const uint32_t*>(v_pages + c);
+      scales[h] = k_pages[s];
+      scales[2 + h] = v_pages[s];
     }
-    *reinterpret_cast<u32x4*>(out + at) = lo;
-    *reinterpret_cast<u32x4*>(out + at + 8) = hi;
-  };
-  put(k_pages, k_out);
-  put(v_pages, v_out);
+  }
+  const int64_t to = (layer * n_rows + t) * kRow + 8 * lane;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    *reinterpret_cast<u32x4*>(k_out + to + 512 * h) = values4(codes[h], scale4(scales[h]));
+    *reinterpret_cast<u32x4*>(v_out + to + 512 * h) = values4(codes[2 + h], scale4(scales[2 + h]));
+  }
 }
 
 }  // namespace
