@@ -2,10 +2,12 @@
 //
 // As append.hip (which says what a token's row and position are), but a row of K or V is stored in the format of
 // cache4.hpp.  K is quantised from its value after norm and rotation, unrounded, V from its bf16 value.
-// K's arithmetic is in fp64 to the code: a value next to a border of two codes comes out on the same side however
+// K's codes are those of fp64 arithmetic: a value next to a border of two codes comes out on the same side however
 // it is computed, so a row's bytes depend on its token alone.
 //
-// One wave takes one token in one layer, 8 lanes a head; four of them hold a block of 32 dims.
+// One wave takes one token in one layer, 8 lanes a head; four of them hold a block of 32 dims.  K is computed in fp32
+// first, with a bound of its error; where the value less and more that bound have different codes, or a block's
+// exponent is open (one wave in a hundred or two), the wave computes its row again in fp64.
 #include "append_core.hpp"
 #include "cache4.hpp"
 #include "msa_kernels.hpp"
@@ -15,16 +17,24 @@ namespace {
 
 constexpr int kAppendWaves = 4;            // tokens per workgroup
 
-template <typename T>
-__device__ __forceinline__ T lanes4_max(T v) {
+// Largest of the four lanes of a block (an aligned quarter of a DPP row).
+__device__ __forceinline__ uint32_t lanes4_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0xB1, 0xF, 0xF, false));     // quad_perm [1,0,3,2]
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x4E, 0xF, 0xF, false));  // quad_perm [2,3,0,1]
+}
+__device__ __forceinline__ double lanes4_max(double v) {
   v = fmax(v, __shfl_xor(v, 1, 64));
   return fmax(v, __shfl_xor(v, 2, 64));
 }
 
-// Exponent of a block whose largest magnitude is m (finite).
+// Exponent of a block whose largest magnitude is m (finite): mantissas up to 1.75 are within 7 * 2^e.
 __device__ __forceinline__ int exponent4(double m) {
   const uint64_t u = (uint64_t)__double_as_longlong(m);
-  const int e = (int)(u >> 52) - 1022 - ((u & 0xFFFFFFFFFFFFFull) <= 0xC000000000000ull ? 3 : 2);
+  const int e = (int)(u >> 52) - 1025 + ((u & 0xFFFFFFFFFFFFFull) > 0xC000000000000ull ? 1 : 0);
+  return e < -125 ? -125 : (e > 125 ? 125 : e);
+}
+__device__ __forceinline__ int exponent4(uint32_t m) {       // of a float's bits
+  const int e = (int)((m + 0x1FFFFFu) >> 23) - 129;
   return e < -125 ? -125 : (e > 125 ? 125 : e);
 }
 
@@ -39,7 +49,7 @@ __device__ __forceinline__ uint32_t quantise8(const double* x, uint32_t* byte) {
     m = fmax(m, a);
   }
   m = lanes4_max(m);
-  odd = lanes4_max(odd ? 1.f : 0.f) > 0.f;
+  odd = lanes4_max(odd ? 1u : 0u) != 0;
   const int e = odd ? 0 : exponent4(m);
   const double unit = __longlong_as_double((long long)(1023 - e) << 52);
   uint32_t w = 0;
@@ -51,6 +61,42 @@ __device__ __forceinline__ uint32_t quantise8(const double* x, uint32_t* byte) {
   }
   *byte = odd ? kNaN4 : (uint32_t)(e + 127);
   return odd ? 0u : w;
+}
+
+__device__ __forceinline__ uint32_t codes8(const float* x, float scale) {
+  uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, x[0], x[1], scale, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2], x[3], scale, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4], x[5], scale, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6], x[7], scale, 3);
+}
+
+// The same in fp32, of values that are off by up to off[i] (null: none): *open where that leaves anything open.  The
+// conversion rounds to the nearest, halfway to the even code, and stops at 6, as the format has it; blocks that hold no
+// numbers, or near fp32's smallest, are left to fp64.
+__device__ __forceinline__ uint32_t quantise8(const float* x, const float* off, uint32_t* byte, bool* open) {
+  uint32_t m = 0, low = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = fabsf(x[i]);
+    m = max(m, __float_as_uint(off ? a + off[i] : a));
+    if (off) low = max(low, __float_as_uint(fmaxf(a - off[i], 0.f)));
+  }
+  m = lanes4_max(m);
+  const int e = exponent4(m);
+  const float scale = __uint_as_float((uint32_t)(e + 127) << 23);
+  *open |= m - 0x0D800000u >= 0x7F800000u - 0x0D800000u;     // below 2^-100, infinite or NaN
+  *byte = (uint32_t)(e + 127);
+  if (!off) return codes8(x, scale);
+  *open |= exponent4(lanes4_max(low)) != e;
+  float lo[8], hi[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    lo[i] = x[i] - off[i];
+    hi[i] = x[i] + off[i];
+  }
+  const uint32_t w = codes8(lo, scale);
+  *open |= w != codes8(hi, scale);
+  return w;
 }
 
 __device__ __forceinline__ double lanes8_sum(double v) {
@@ -84,68 +130,101 @@ append4_kernel(int32_t B, int32_t n_q, int32_t Hq, const uint16_t* __restrict__ 
     const int32_t p = page_table[(int64_t)b * max_pages + (row >> page_shift)];
     if (p >= 0 && p < n_pages) page = ((layer * n_pages + p) << page_shift) * kRow4;
   }
+  float cs[8], sn[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    cs[i] = 1.f;
+    sn[i] = 0.f;
+  }
+  if (turn) angles(pos, j, pw, cs, sn);
   if (page >= 0) {
     const int64_t at = (layer * n_q + t) * kRow + head * kDim + 8 * j;
+    const int r = (int)(row & ((1 << page_shift) - 1));
+    auto store = [&](uint8_t* pages, const uint32_t* w, const uint32_t* byte) {
+      uint8_t* codes = pages + page + codes4_at(head, r, page_shift) + 4 * j;
+      *reinterpret_cast<uint32_t*>(codes) = w[0];
+      *reinterpret_cast<uint32_t*>(codes + 32) = w[1];
+      uint8_t* scales = pages + page + scales4_at(head, r, page_shift) + (j >> 2);
+      if ((j & 3) == 0) {
+        scales[0] = (uint8_t)byte[0];
+        scales[2] = (uint8_t)byte[1];
+      }
+    };
+    const u32x4 k_lo = *reinterpret_cast<const u32x4*>(k_new + at), k_hi = *reinterpret_cast<const u32x4*>(k_new + at + 64);
+    const u32x4 v_lo = *reinterpret_cast<const u32x4*>(v_new + at), v_hi = *reinterpret_cast<const u32x4*>(v_new + at + 64);
     float f[16], w[16];
-    double x[16];
-    unpack8(*reinterpret_cast<const u32x4*>(k_new + at), f);
-    unpack8(*reinterpret_cast<const u32x4*>(k_new + at + 64), f + 8);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = f[i];
+    uint32_t code[2], byte[2];
+    bool open = false;
+    unpack8(k_lo, f);
+    unpack8(k_hi, f + 8);
+    double inv = 1.0;
     if (NORM_K) {
       unpack8(*reinterpret_cast<const u32x4*>(w_k + layer * kDim + 8 * j), w);
       unpack8(*reinterpret_cast<const u32x4*>(w_k + layer * kDim + 64 + 8 * j), w + 8);
       double ss = 0.0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) ss += x[i] * x[i];
-      const double inv = 1.0 / sqrt(lanes8_sum(ss) * (1.0 / kDim) + (double)eps);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] *= inv * (double)w[i];
+      for (int i = 0; i < 16; ++i) ss += (double)f[i] * (double)f[i];
+      inv = 1.0 / sqrt(lanes8_sum(ss) * (1.0 / kDim) + (double)eps);
     }
-    if (turn) {
-      double fr = (j & 1 ? pw.r8 : 1.0) * (j & 2 ? pw.r16 : 1.0) * (j & 4 ? pw.r32 : 1.0) * 0.15915494309189533577;
+    {
+      // With u = 2^-24: a value after the norm is off by 1.5 u of itself (inv, inv w, the product), a cosine or sine by
+      // 1.6 u (its angle's rounding) and two steps, 2 u; a value turned by their sums in both products, 5.1 u, a product's
+      // rounding and its own: under 7 u (|a| + |b|).  12 u here.
+      float x[16], off[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const double turns = pos * fr;
-        double sn, cs;
-        sincospi(2.0 * (turns - rint(turns)), &sn, &cs);
-        fr *= pw.r1;
-        const double lo = x[i] * cs - x[i + 8] * sn, hi = x[i + 8] * cs + x[i] * sn;
-        x[i] = lo;
-        x[i + 8] = hi;
+        float a = f[i], b = f[i + 8];
+        if (NORM_K) {
+          a *= (float)inv * w[i];
+          b *= (float)inv * w[i + 8];
+        }
+        off[i] = (fabsf(a) + fabsf(b)) * (NORM_K || turn ? 12 * 0x1p-24f : 0.f);
+        x[i] = turn ? a * cs[i] - b * sn[i] : a;
+        x[i + 8] = turn ? b * cs[i] + a * sn[i] : b;
       }
+      code[0] = quantise8(x, off, byte, &open);
+      code[1] = quantise8(x + 8, off, byte + 1, &open);
     }
-    const int r = (int)(row & ((1 << page_shift) - 1));
-    auto store = [&](uint8_t* pages) {
-      uint32_t s_lo, s_hi;
-      const uint32_t lo = quantise8(x, &s_lo), hi = quantise8(x + 8, &s_hi);
-      uint8_t* codes = pages + page + codes4_at(head, r, page_shift) + 4 * j;
-      *reinterpret_cast<uint32_t*>(codes) = lo;
-      *reinterpret_cast<uint32_t*>(codes + 32) = hi;
-      uint8_t* scales = pages + page + scales4_at(head, r, page_shift) + (j >> 2);
-      if ((j & 3) == 0) {
-        scales[0] = (uint8_t)s_lo;
-        scales[2] = (uint8_t)s_hi;
-      }
-    };
-    store(k_pages);
-    unpack8(*reinterpret_cast<const u32x4*>(v_new + at), f);
-    unpack8(*reinterpret_cast<const u32x4*>(v_new + at + 64), f + 8);
+    if (__ballot(open)) {
+      double x[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = f[i];
-    store(v_pages);
+      for (int i = 0; i < 16; ++i) x[i] = NORM_K ? (double)f[i] * (inv * (double)w[i]) : (double)f[i];
+      if (turn) {
+        double fr = (j & 1 ? pw.r8 : 1.0) * (j & 2 ? pw.r16 : 1.0) * (j & 4 ? pw.r32 : 1.0) * 0.15915494309189533577;
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const double turns = pos * fr;
+          double s, c;
+          sincospi(2.0 * (turns - rint(turns)), &s, &c);
+          fr *= pw.r1;
+#pragma unroll
+          for (int n = 0; n < 8; ++n)               // registers have no index
+            if (n == i) {
+              const double lo = x[n] * c - x[n + 8] * s, hi = x[n + 8] * c + x[n] * s;
+              x[n] = lo;
+              x[n + 8] = hi;
+            }
+        }
+      }
+      code[0] = quantise8(x, byte);
+      code[1] = quantise8(x + 8, byte + 1);
+    }
+    store(k_pages, code, byte);
+    unpack8(v_lo, f);
+    unpack8(v_hi, f + 8);
+    open = false;
+    code[0] = quantise8(f, nullptr, byte, &open);
+    code[1] = quantise8(f + 8, nullptr, byte + 1, &open);
+    if (__ballot(open)) {
+      double x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = (double)f[i];
+      code[0] = quantise8(x, byte);
+      code[1] = quantise8(x + 8, byte + 1);
+    }
+    store(v_pages, code, byte);
   }
   if (q) {
-    float cs[8], sn[8];
-    if (turn) {
-      angles(pos, j, pw, cs, sn);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        cs[i] = 1.f;
-        sn[i] = 0.f;
-      }
-    }
     float w_lo[8], w_hi[8];
     if (NORM_Q) {
       unpack8(*reinterpret_cast<const u32x4*>(w_q + layer * kDim + 8 * j), w_lo);
