@@ -159,6 +159,23 @@ def test_norm_and_turn_of_odd_rows():
     assert (scales[0, page, at, 5] == 255).all() and (scales[0, page, at, 4] < 255).all()
 
 
+@pytest.mark.parametrize("up,down", [(120, -20), (125, -30), (100, -28), (-60, 100), (127, 0)])
+def test_norm_of_keys_whose_factor_is_below_the_smallest_float(up, down):
+    """Large keys with small weights: 1 / rms times a weight is below fp32's normal numbers, the key that it makes is
+    not."""
+    print("case: append4 of keys times 2^%d, weights times 2^%d" % (up, down), flush=True)
+    b = Batch4([40], [40], page=8, hq=8, layers=1, seed=10)
+    b.k_new = (b.k_new.float().clamp(-1.9, 1.9) * 2.0 ** up).to(BF16)
+    b.w_k = (b.w_k.float() * 2.0 ** down).to(BF16)
+    d = b.to_device()
+    append(b, d, eps=0.0)
+    want = {}
+    for i in range(40):
+        x, size = turned(b.k_new[0, i:i + 1], b.w_k[0], [i], eps=0.0)
+        want[0, 0, i] = x[0], size[0]
+    check_pages(b, b.k_pages4, d["k_pages"].cpu(), want, 2.0 ** -40)
+
+
 def test_rows_without_a_place_are_not_stored():
     """Local rows below 0, past the table and on pages that are none; their q is turned all the same."""
     print("case: append4 without a place", flush=True)
