@@ -10,8 +10,8 @@
 //   are loaded as the first product's A operand takes them (lane l: 32 dims, a block with its scale, of row l & 15) and
 //   turned into bf16 in registers; V's codes wait in the wave's LDS tile, so that their registers take the next
 //   tile's, and are turned into bf16 there 32 rows at a time.  Bound: HBM.  One token over 36,300 rows in 18 layers:
-//   209 us, 4.4 TB/s; 64 users' long conversations in one layer: 94 us, 4.0 TB/s.  A second tile of K on its way takes
-//   registers that are not there (232-278 us).
+//   201 us, 4.6 TB/s; 64 users' long conversations in one layer: 95 us, 4.0 TB/s.  A second tile of K on its way takes
+//   registers that are not there (232-278 us for then 209).
 // - More columns: 4 waves share tiles of 32 rows, which are turned into bf16 on the way into LDS, four tiles a step,
 //   the next step's codes on their way meanwhile (loaded when they are needed: 273 us where this takes 141,
 //   drafted tokens).  Bound: matrix and vector units in turn.
@@ -24,8 +24,12 @@
 namespace msa {
 namespace {
 
+// Costs: where all shares had as many tiles, those of memory rows ended after 128 us, those of local ones (four times
+// the softmax, and codes to turn) after 173 to 231; one token over 4,300 + 32,000 rows in 18 layers 201 us, 217 with equal
+// costs, 207 with 3 to 4, 202 with 3 to 5, 213 with 1 to 2.
 struct Rows4 {
-  static constexpr int kStreamCtx = 16, kStreamLocal = 64;
+  static constexpr int kStreamCtx = 16, kStreamLocal = 64, kCtxCost = 2, kLocalCost = 3;
+  static constexpr bool kLongestFirst = true;
 };
 
 // A share of the streams; `tile` is the wave's.
@@ -566,7 +570,15 @@ attend4_kernel(const AttendArgs a) {
     attend_streams<BF16_OUT>(a, n, p, sh.streams.seg, sh.streams.n_seg, reinterpret_cast<uint16_t*>(tile),
                              id - first_share, layer, tid);
   } else if (id >= first_item && id < first_item + p.all_items) {
-    find_item(a, n, p, sh.item.item, id - first_item, tid);
+    // Items of one round, two a CU (workgroup i and i + the number of CUs): the longest that need not share have a CU each, of
+    // the others the longest and the shortest are side by side.  CUs then end within 85 to 98 us, 59 to 124 without.
+    uint32_t item = id - first_item;
+    const uint32_t cus = a.wgs / 2, n_items = p.all_items;
+    if (p.all_cost == 0 && n_items > cus && n_items <= 2 * cus) {
+      const uint32_t alone = 2 * cus - n_items;
+      item = item < cus - alone ? item + alone : (item < cus ? item - (cus - alone) : n_items - 1 - (item - cus));
+    }
+    find_item(a, n, p, sh.item.item, item, tid);
     if (sh.item.item.valid) attend_item<BF16_OUT>(a, n, sh.item, stage0, stage1, stage2, stage3, layer, tid);
   }
 }

@@ -91,6 +91,7 @@ struct Lengths {
   // bit b: sequence b shares rows with none before it (first of its group, alone, or behind one that is)
   uint32_t* start;                // [kMaxSeqs / 32 + 1]
   uint32_t* sums;                 // [8][kWaves]
+  int4* items;                    // [kThreads]: of each job, where a thread has one at most
   bool grouped;                   // whether any sequence may share: not where each is its own group
 };
 constexpr int kStartWords = kMaxSeqs / 32 + 1;
@@ -105,6 +106,7 @@ __device__ __forceinline__ Lengths lengths_in(u32x4* a, u32x4* b, u32x4* c, u32x
   n.grp = reinterpret_cast<int32_t*>(d);
   n.start = reinterpret_cast<uint32_t*>(n.off + kMaxSeqs + 4);
   n.sums = n.start + kStartWords + 3;
+  n.items = reinterpret_cast<int4*>(n.clen + kMaxSeqs);
   n.grouped = false;
   return n;
 }
@@ -210,9 +212,11 @@ __device__ __forceinline__ Job job_of(const AttendArgs& a, const Lengths& n, int
   return x;
 }
 
-// How a cache holds its local rows: the rows of a streamed tile, memory rows (always bf16) and local ones.
+// How a cache holds its local rows: the rows of a streamed tile, memory rows (always bf16) and local ones, what
+// either tile costs, and whether a layer's longest items come first.
 struct RowsBf16 {
-  static constexpr int kStreamCtx = kStreamRows, kStreamLocal = kStreamRows;
+  static constexpr int kStreamCtx = kStreamRows, kStreamLocal = kStreamRows, kCtxCost = 1, kLocalCost = 1;
+  static constexpr bool kLongestFirst = false;
 };
 
 // Tiles: t memory rows each, then `local` local rows each; one for a job without rows (its columns are zero).
@@ -220,9 +224,22 @@ __device__ __forceinline__ int32_t ctx_tiles(const Job& x, int32_t t) { return (
 __device__ __forceinline__ int32_t tiles_of(const Job& x, int32_t t, int32_t local) {
   return max(1, ctx_tiles(x, t) + (max(0, x.p1 - x.p0) + local - 1) / local);
 }
+__device__ __forceinline__ int32_t item_tiles(const Job& x) { return tiles_of(x, kTileRows, kTileRows); }
+
+// Cost of a stream's first t tiles, of all of them, and the first tile behind a cost.
+template <class F>
+__device__ __forceinline__ uint32_t stream_cost(const Job& x, int32_t t) {
+  const int32_t c = min(t, ctx_tiles(x, F::kStreamCtx));
+  return (uint32_t)(c * F::kCtxCost + (t - c) * F::kLocalCost);
+}
 template <class F>
 __device__ __forceinline__ int32_t stream_tiles(const Job& x) { return tiles_of(x, F::kStreamCtx, F::kStreamLocal); }
-__device__ __forceinline__ int32_t item_tiles(const Job& x) { return tiles_of(x, kTileRows, kTileRows); }
+template <class F>
+__device__ __forceinline__ int32_t tile_behind(const Job& x, uint32_t cost) {
+  const uint32_t c = ctx_tiles(x, F::kStreamCtx);
+  return (int32_t)(cost <= c * F::kCtxCost ? (cost + F::kCtxCost - 1) / F::kCtxCost
+                                           : c + (cost - c * F::kCtxCost + F::kLocalCost - 1) / F::kLocalCost);
+}
 
 // Keeps a uniform value in scalar registers: the compiler would rather load kernel arguments again in every
 // tile, and wait for them.
@@ -543,8 +560,8 @@ __device__ __forceinline__ void describe(const AttendArgs& a, const Job& x, cons
 // ------------------------------------------------------------------ who does what
 //
 // Streamed jobs make two streams of rows each, one for each set of 4 heads (a wave each).  All streams of
-// a layer are laid end to end and cut into equal shares, one for each workgroup: every one has the same
-// number of tiles whatever the lengths are, and one start.  A share holds pieces of one or more
+// a layer are laid end to end and cut into equal shares, one for each workgroup: every one has tiles of the same
+// cost whatever the lengths are, and one start.  A share holds pieces of one or more
 // streams; a piece is one part of its columns.
 //
 // The other jobs make items: a column block of 128, one head, a chunk of the rows.  A job's rows are cut
@@ -552,7 +569,9 @@ __device__ __forceinline__ void describe(const AttendArgs& a, const Job& x, cons
 // sequences behind 30,000 shared rows take 140 us, so 118), but into chunks of eight tiles at least
 // (four or sixteen measure the same).  Of a job's items those of the last column blocks, whose tokens see the most rows,
 // come first (workgroups start in order); heads fastest (workgroups go to the 8 XCDs in turn: a
-// head's rows stay in one L2).
+// head's rows stay in one L2).  Rows in 4 bits: jobs with longer items come first, and what the rounding down leaves of the
+// workgroups goes to the longest (24 sequences of five drafted tokens and 100 to 9,000 rows: 127 us in the jobs' order, 119
+// sorted and paired as below, 108 with those chunks; the mixed batch 254 and 241).
 
 __device__ __forceinline__ bool streamed(const Job& x) { return x.cols <= kStreamCols; }
 
@@ -574,9 +593,10 @@ __device__ __forceinline__ int32_t units_of(const Job& x) {
 struct Plan {
   int32_t j0, j1;                 // this thread's jobs
   Job first;                      // the first of them (mostly the only one)
-  uint32_t tiles, streams;        // of streamed jobs before them
+  uint32_t cost, streams;         // of streamed jobs before them
   uint32_t items, units;          // items, and units of those that are parts, before them
-  uint32_t all_tiles, all_items, share, shares;    // tiles of a share, shares
+  uint32_t all_cost, all_items, share, shares;     // cost of a share, shares
+  int32_t more;                   // chunks of this thread's only job on top of chunks_of
   float aim;
 };
 
@@ -588,48 +608,87 @@ __device__ __forceinline__ Plan make_plan(const AttendArgs& a, const Lengths& n,
   p.j1 = min(nj, p.j0 + per);
   p.first.cols = 0;
   if (p.j0 < p.j1) p.first = job_of(a, n, p.j0);
-  // tiles of a layer's streams fit 32 bits: 2 x 4,096 streams of at most 2 x 2^17 tiles.  Work of the
-  // items: fp32 sum of whole numbers, in the same order in every workgroup
-  uint32_t tiles = 0, streams = 0, all[2];
+  // the cost of a layer's streams fits 32 bits: 2 x 4,096 streams of at most 2^17 tiles of local rows (2^16 in 4 bits),
+  // and memory rows, which fit the card.  Work of the items: fp32 sum of whole numbers, in the same order in every
+  // workgroup
+  uint32_t cost = 0, streams = 0, all[2];
   float work = 0.f;
   for (int32_t j = p.j0; j < p.j1; ++j) {
     const Job x = j == p.j0 ? p.first : job_of(a, n, j);
     if (x.cols == 0) continue;
     if (streamed(x)) {
-      tiles += kSets * stream_tiles<F>(x);
+      cost += kSets * stream_cost<F>(x, stream_tiles<F>(x));
       streams += kSets;
     } else {
       work += (float)item_tiles(x) * (float)items_of(x);
     }
   }
-  p.tiles = tiles;
+  p.cost = cost;
   p.streams = streams;
   work = wave_sum(work);
   float* sums = reinterpret_cast<float*>(n.sums + 4 * kWaves);
   if ((tid & 63) == 0) sums[tid >> 6] = work;
-  scan2(n, 0, tiles, streams, all, tid);
-  p.tiles = tiles - p.tiles;
+  // jobs with items, where a thread has one at most: how many, and this thread's place among them
+  const bool own = F::kLongestFirst && nj <= kThreads && p.j0 < p.j1 && p.first.cols > 0 && !streamed(p.first);
+  const uint64_t owners = __ballot(own);
+  int32_t n_own = 0, at = __builtin_popcountll(owners & ((1ull << (tid & 63)) - 1));
+  if ((tid & 63) == 0) n.sums[5 * kWaves + (tid >> 6)] = (uint32_t)__builtin_popcountll(owners);
+  scan2(n, 0, cost, streams, all, tid);
+  p.cost = cost - p.cost;
   p.streams = streams - p.streams;
-  p.all_tiles = all[0];
+  p.all_cost = all[0];
   work = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) work += sums[w];
+  for (int w = 0; w < kWaves; ++w) {
+    work += sums[w];
+    const int32_t c = (int32_t)n.sums[5 * kWaves + w];
+    n_own += c;
+    at += w < tid >> 6 ? c : 0;
+  }
   p.all_items = p.items = p.units = 0;
+  p.more = 0;
   p.aim = 0.f;
   p.shares = a.wgs;
   if (work > 0.f) {                               // uniform
     // a streamed tile is 4 heads' rows, an item's is one head's, of more columns: 4.2 against 1.2 us where
     // both wait for HBM, 2.3 against 1.2 next to items bound by the matrix cores (2, 3 and 4 in place of
     // one for the other measure the same within 3%)
-    const float streams_work = 3.f * (float)p.all_tiles;
-    const int32_t wgs = p.all_tiles ? a.both_wgs : a.wgs;
+    const float streams_work = 3.f / F::kLocalCost * (float)p.all_cost;
+    const int32_t wgs = p.all_cost ? a.both_wgs : a.wgs;
     // 2^-10 below: the roundings of the sum
     p.aim = wgs * (1.f - 0x1p-10f) / (work + streams_work);
+    uint32_t ahead = 0;
+    if (n_own > 1) {                              // uniform
+      // Longest items first, those of one length in the jobs' order.  A tile costs about 1 + column blocks.
+      int32_t nch = own ? chunks_of(p.first, p.aim) : 0;
+      const int32_t k = own ? items_of(p.first) : 0, t = own ? item_tiles(p.first) : 0;
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
+        const int32_t length = own ? (t + nch - 1) / nch * (1 + blocks_of(p.first.cols)) : 0;
+        if (own) n.items[at] = make_int4(length, nch * k, k, 0);
+        __syncthreads();
+        uint32_t total = 0, chunks = 0;           // all items; one chunk of each of those ahead
+        ahead = 0;
+#pragma unroll 4
+        for (int32_t i = 0; i < n_own; ++i) {
+          const int4 o = n.items[i];
+          const bool first = o.x > length || (o.x == length && i < at);
+          total += o.y;
+          ahead += first ? o.y : 0;
+          chunks += first ? o.z : 0;
+        }
+        // workgroups that the rounding down leaves: a chunk more for the longest
+        if (pass > 0 || p.all_cost > 0 || total >= (uint32_t)wgs) break;      // uniform
+        if (own && total + chunks + k <= (uint32_t)wgs && t / 8 > nch) p.more = 1;
+        nch += p.more;
+        __syncthreads();
+      }
+    }
     uint32_t items = 0, units = 0;
     for (int32_t j = p.j0; j < p.j1; ++j) {
       const Job x = j == p.j0 ? p.first : job_of(a, n, j);
       if (x.cols == 0 || streamed(x)) continue;
-      const int32_t nch = chunks_of(x, p.aim);
+      const int32_t nch = chunks_of(x, p.aim) + p.more;
       const uint32_t k = nch * items_of(x);
       items += k;
       if (x.shared || x.split || nch > 1) units += nch * units_of(x);
@@ -637,13 +696,15 @@ __device__ __forceinline__ Plan make_plan(const AttendArgs& a, const Lengths& n,
     p.items = items;
     p.units = units;
     scan2(n, 1, items, units, all, tid);
-    p.items = items - p.items;
+    p.items = n_own > 1 ? ahead : items - p.items;
     p.units = units - p.units;
     p.all_items = all[0];
     p.shares = max((int32_t)(streams_work * p.aim), wgs - (int32_t)min(p.all_items, (uint32_t)wgs));
-    p.shares = p.all_tiles ? max(p.shares, 1u) : 0u;
+    p.shares = p.all_cost ? max(p.shares, 1u) : 0u;
   }
-  p.share = p.shares ? max(1u, (p.all_tiles + p.shares - 1) / p.shares) : 1u;
+  // a tile is of the share that its cost begins in: none between a stream's first and last is without one
+  constexpr uint32_t least = F::kCtxCost > F::kLocalCost ? F::kCtxCost : F::kLocalCost;
+  p.share = p.shares ? max(least, (p.all_cost + p.shares - 1) / p.shares) : least;
   return p;
 }
 
@@ -663,47 +724,46 @@ struct Segment {
   Parts parts;
 };
 
-// The pieces of streams in share `number`, from tile `from` of the layer's on: up to kSegments into `seg`, their
+// The pieces of streams in share `number`, from cost `from` of the layer's on: up to kSegments into `seg`, their
 // number in n_seg[0]; returns where the list ends, 0 where that is the share's end.
 template <class F>
 __device__ __forceinline__ uint32_t list_segments(const AttendArgs& a, const Lengths& n, const Plan& p, Segment* seg,
                                                   uint32_t* n_seg, uint32_t number, uint32_t from) {
   const uint32_t share = p.share;
   const uint64_t begin = (uint64_t)number * share;
-  if (begin >= p.all_tiles) return 0;
+  if (begin >= p.all_cost) return 0;
   from = max(from, (uint32_t)begin);
-  const uint32_t to = min((uint32_t)begin + share, p.all_tiles);
+  const uint32_t to = (uint32_t)min(begin + share, (uint64_t)p.all_cost);
   auto walk = [&](auto&& f) __attribute__((always_inline)) {
-    uint32_t u = p.tiles, s = p.streams;
+    uint32_t u = p.cost, s = p.streams;
     for (int32_t j = p.j0; j < p.j1 && u < to; ++j) {
       const Job x = j == p.j0 ? p.first : job_of(a, n, j);
       if (x.cols == 0 || !streamed(x)) continue;
-      const uint32_t t = stream_tiles<F>(x);
+      const int32_t tiles = stream_tiles<F>(x);
+      const uint32_t t = stream_cost<F>(x, tiles), last = stream_cost<F>(x, tiles - 1);     // where the last tile begins
       for (int set = 0; set < kSets; ++set, u += t, ++s)
-        if (u < to && u + t > from) f(x, set, u, t, s);
+        if (u < to && u + last >= from) f(x, set, u, t, last, s);
     }
   };
-  // the stream that holds `from` is the list's first
-  walk([&](const Job&, int, uint32_t u, uint32_t, uint32_t s) {
-    if (u <= from) n_seg[1] = s;
-  });
+  // the first stream with a tile that begins at `from` or behind it is the list's first
+  walk([&](const Job&, int, uint32_t, uint32_t, uint32_t, uint32_t s) { atomicMax(n_seg + 1, ~s); });
   __syncthreads();
-  const uint32_t s_first = n_seg[1];
-  walk([&](const Job& x, int set, uint32_t u, uint32_t t, uint32_t s) {
+  const uint32_t s_first = ~n_seg[1];
+  walk([&](const Job& x, int set, uint32_t u, uint32_t t, uint32_t last, uint32_t s) {
     const uint32_t k = s - s_first;
     if (k >= kSegments) return;
     Segment& g = seg[k];
     g.x = x;
     g.set = set;
-    g.tile0 = (int32_t)(max(from, u) - u);
-    g.tile1 = (int32_t)(min(to, u + t) - u);
+    g.tile0 = tile_behind<F>(x, max(from, u) - u);
+    g.tile1 = tile_behind<F>(x, min(to, u + t) - u);
     g.first = set == 0 && g.tile0 == 0;
     g.limit0 = visible_rows(n.len[x.seq], n.off[x.seq + 1], x.t0) - x.p0;
     // the stream's tiles lie in shares w0 .. w1; stream + share number is a number of its own for every
     // piece, consecutive along a stream
     bool whole = true;
     for (int v = 0; v < kSets; ++v) {
-      const uint32_t u0 = u + (v - set) * t, w0 = u0 / share, w1 = (u0 + t - 1) / share;
+      const uint32_t u0 = u + (v - set) * t, w0 = u0 / share, w1 = (u0 + last) / share;
       g.parts.first[v] = (int32_t)(kWaves * (w0 + s + v - set));
       g.parts.parts[v] = (int32_t)(w1 - w0 + 1);
       if (w1 > w0) whole = false;
@@ -737,7 +797,7 @@ __device__ __forceinline__ void find_item(const AttendArgs& a, const Lengths& n,
   for (int32_t j = p.j0; j < p.j1 && at <= id; ++j) {
     const Job x = j == p.j0 ? p.first : job_of(a, n, j);
     if (x.cols == 0 || streamed(x)) continue;
-    const int32_t nch = chunks_of(x, p.aim), ncb = items_of(x) / kHeads;
+    const int32_t nch = chunks_of(x, p.aim) + p.more, ncb = items_of(x) / kHeads;
     const uint32_t k = nch * ncb * kHeads;
     const bool parts = x.shared || x.split || nch > 1;
     if (id < at + k) {

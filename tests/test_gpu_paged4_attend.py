@@ -167,6 +167,32 @@ def test_many_sequences():
     check(b, attend(b))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("sequences,layers", [(2, 1), (9, 1), (24, 2), (24, 18), (70, 1), (130, 2), (257, 1)])
+def test_order_of_items(sequences, layers, dtype):
+    """Wide sequences of ragged lengths: fewer items than compute units, one round of them with and without chunks to
+    spare, several rounds, more sequences than threads of a plan."""
+    print("case: order of items", sequences, layers, dtype, flush=True)
+    rng = np.random.default_rng(sequences)
+    new = [int(rng.choice([5, 5, 9, 0])) if s else 5 for s in range(sequences)]
+    rows = [n + int(rng.integers(0, 3000 if sequences < 30 else 300)) for n in new]
+    b = Batch4(new, rows, page=16, hq=64, layers=layers, seed=400 + sequences)
+    check(b, attend(b, dtype=dtype))
+
+
+@pytest.mark.parametrize("layers", [1, 7, 18])
+@pytest.mark.parametrize("most", [3, 40, 300])
+def test_shares_end_anywhere_in_memory_and_local_rows(most, layers):
+    """Short streams of memory rows and local ones, which cost unlike: shares that end with a tile, in one, and with a stream."""
+    print("case: shares of memory and local rows", most, layers, flush=True)
+    rng = np.random.default_rng(most)
+    new = [1] * 45
+    rows = [1 + int(rng.integers(0, most)) for _ in new]
+    ctx = rng.integers(0, most + 1, (layers, 45)).tolist()
+    b = Batch4(new, rows, ctx=ctx, page=16, hq=16, layers=layers, seed=500 + most)
+    check(b, attend(b))
+
+
 @pytest.mark.parametrize("grouped", [False, True])
 def test_shares_of_many_pieces(grouped):
     """More pieces in a workgroup's share of the rows than it lists at a time, next to shared tiles."""
