@@ -13,8 +13,8 @@
 //   201 us, 4.6 TB/s; 64 users' long conversations in one layer: 95 us, 4.0 TB/s.  A second tile of K on its way takes
 //   registers that are not there (232-278 us for then 209).
 // - More columns: 4 waves share tiles of 32 rows, which are turned into bf16 on the way into LDS, four tiles a step,
-//   the next step's codes on their way meanwhile (loaded when they are needed: 273 us where this takes 141,
-//   drafted tokens).  Bound: matrix and vector units in turn.
+//   the next step's codes on their way meanwhile (loaded when they are needed: 273 us where this took 141,
+//   drafted tokens; 102-109 now).  Bound: matrix and vector units in turn.
 // - Four column blocks, over tiles that all columns see: a pipeline of its own, where each wave forms the next tile's
 //   scores beside this one's weights.  4,000 tokens over 32,300 rows: 2.16 ms, 1.04 PFLOP/s, matrix cores 47% busy while
 //   the clock falls to 2.07 GHz; 2.36 ms without it.  For two blocks it gains nothing.
