@@ -443,8 +443,8 @@ int msa_paged_attend(int32_t n_layers, int32_t B, int32_t n_groups, int32_t n_q,
 /* msa_paged_append into a cache in 4 bits.  K is quantised from its value after norm and rotation before any rounding
  * (computed in fp64 wherever fp32 leaves a code open: a row's bytes depend on its token alone), V from its bf16
  * value; q is normed and turned in fp32 with one rounding to bf16, as msa_paged_append does.  theta == 0: no
- * rotation (rows that are in position, of a cache in bf16 say; with w_k and w_q NULL they are
- * quantised as they are).  Arguments, tokens that are not stored and errors else as msa_paged_append. */
+ * rotation (rows that are in position, of a cache in bf16 say): no dim reaches another but through a norm, infinities
+ * and NaN included; without w_k keys are quantised as they are, without w_q q_out holds q's bits.  Arguments, tokens that are not stored and errors else as msa_paged_append. */
 int msa_paged_append4(int32_t n_layers, int32_t B, int32_t n_q, int32_t Hq, const uint16_t* k_new,
                       const uint16_t* v_new, const uint16_t* q, const int32_t* q_off, const int32_t* kv_len,
                       const int32_t* pos_off, const int32_t* page_table, int32_t max_pages, int32_t page_tokens,

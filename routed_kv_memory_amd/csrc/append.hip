@@ -54,7 +54,7 @@ append_kernel(int32_t B, int32_t n_q, int32_t Hq, const uint16_t* __restrict__ k
     unpack8(*reinterpret_cast<const u32x4*>(w_k + layer * kDim + 8 * j), w_lo);
     unpack8(*reinterpret_cast<const u32x4*>(w_k + layer * kDim + 64 + 8 * j), w_hi);
   }
-  norm_turn<NORM_K>(k_lo, k_hi, w_lo, w_hi, eps, cs, sn);
+  norm_turn<NORM_K>(k_lo, k_hi, w_lo, w_hi, eps, true, cs, sn);
   if (row >= 0 && (row >> page_shift) < max_pages) {
     const int32_t page = page_table[(int64_t)b * max_pages + (row >> page_shift)];
     if (page >= 0 && page < n_pages) {
@@ -76,7 +76,7 @@ append_kernel(int32_t B, int32_t n_q, int32_t Hq, const uint16_t* __restrict__ k
     for (int32_t h = 0; h < Hq; h += 8) {   // q_out may be q: a lane writes only what it has read
       u32x4 lo = *reinterpret_cast<const u32x4*>(q + q_at + h * kDim);
       u32x4 hi = *reinterpret_cast<const u32x4*>(q + q_at + h * kDim + 64);
-      norm_turn<NORM_Q>(lo, hi, w_lo, w_hi, eps, cs, sn);
+      norm_turn<NORM_Q>(lo, hi, w_lo, w_hi, eps, true, cs, sn);
       *reinterpret_cast<u32x4*>(q_out + q_at + h * kDim) = lo;
       *reinterpret_cast<u32x4*>(q_out + q_at + h * kDim + 64) = hi;
     }

@@ -241,7 +241,7 @@ append4_kernel(int32_t B, int32_t n_q, int32_t Hq, const uint16_t* __restrict__ 
     for (int32_t h = 0; h < Hq; h += 8) {   // q_out may be q: a lane writes only what it has read
       u32x4 lo = *reinterpret_cast<const u32x4*>(q + q_at + h * kDim);
       u32x4 hi = *reinterpret_cast<const u32x4*>(q + q_at + h * kDim + 64);
-      norm_turn<NORM_Q>(lo, hi, w_lo, w_hi, eps, cs, sn);
+      norm_turn<NORM_Q>(lo, hi, w_lo, w_hi, eps, turn, cs, sn);
       *reinterpret_cast<u32x4*>(q_out + q_at + h * kDim) = lo;
       *reinterpret_cast<u32x4*>(q_out + q_at + h * kDim + 64) = hi;
     }

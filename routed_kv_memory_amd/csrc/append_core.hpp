@@ -44,10 +44,12 @@ __device__ __forceinline__ float lanes8_sum(float v) {
   return v + __int_as_float(__builtin_amdgcn_update_dpp(x, x, 0x141, 0xF, 0xF, false));   // row_half_mirror
 }
 
-// One head's row in 8 lanes: lo = dims 8 j .., hi = dims 64 + 8 j ..; normed (w != NULL) and turned.
+// One head's row in 8 lanes: lo = dims 8 j .., hi = dims 64 + 8 j ..; normed (w != NULL) and turned (`turn`).  A turn
+// by nothing is left out, not computed: 0 times an infinity is NaN, and the sum of -0 and 0 is 0.
 template <bool NORM>
-__device__ __forceinline__ void norm_turn(u32x4& lo, u32x4& hi, const float* w_lo, const float* w_hi, float eps,
+__device__ __forceinline__ void norm_turn(u32x4& lo, u32x4& hi, const float* w_lo, const float* w_hi, float eps, bool turn,
                                           const float* cs, const float* sn) {
+  if (!NORM && !turn) return;
   float a[8], b[8];
   unpack8(lo, a);
   unpack8(hi, b);
@@ -65,8 +67,8 @@ __device__ __forceinline__ void norm_turn(u32x4& lo, u32x4& hi, const float* w_l
   float x[8], y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    x[i] = a[i] * cs[i] - b[i] * sn[i];
-    y[i] = b[i] * cs[i] + a[i] * sn[i];
+    x[i] = turn ? a[i] * cs[i] - b[i] * sn[i] : a[i];
+    y[i] = turn ? b[i] * cs[i] + a[i] * sn[i] : b[i];
   }
   lo = pack8(x);
   hi = pack8(y);

@@ -138,6 +138,36 @@ def test_rows_as_they_are():
     assert v[0].isnan().sum() == 8 * 64 == k[0].isnan().sum()          # the two blocks of each head, no others
 
 
+@pytest.mark.parametrize("norm", ["", "q"])
+@pytest.mark.parametrize("hq", [8, 64])
+def test_no_rotation_takes_no_dim_to_another(norm, hq):
+    """theta 0 and queries with infinities, NaN and zeros of either sign: without a norm the bits of q, with one each
+    dim by itself."""
+    print("case: append4 without rotation, odd queries", norm, hq, flush=True)
+    b = Batch4([9], [9], page=4, hq=hq, layers=2, seed=16)
+    inf, nan = float("inf"), float("nan")
+    q = b.q
+    q[:, 0] = -0.0
+    q[:, 1, :, 3], q[:, 2, :, 70], q[:, 3, :, 5] = inf, -inf, nan
+    q[:, 4, :, 9], q[:, 4, :, 73] = inf, -inf               # both of a pair that a rotation would turn
+    q[:, 5, :, :64], q[:, 6, :, 64:] = -0.0, -0.0
+    q[:, 7] = q[:, 7].abs().neg()
+    q[:, 7, :, :64] = -0.0                                  # -0 beside negative partners
+    d = b.to_device()
+    got = append(b, d, norm=norm, theta=0.0).cpu()
+    if not norm:
+        assert torch.equal(got.view(torch.int16), q.view(torch.int16))
+        return
+    x = q.double()
+    want = x / torch.sqrt((x * x).mean(-1, keepdim=True) + float(np.float32(EPS))) * b.w_q.double()[:, None, None]
+    assert torch.equal(got.isnan(), want.isnan())           # of a head with infinities those alone, with a NaN all
+    ok = ~want.isnan()
+    assert torch.equal(torch.signbit(got)[ok], torch.signbit(want)[ok])
+    # fp32: 16 squares summed in a lane, 3 sums over lanes, mean, eps, root, 1 / it (2 steps each), two products; then bf16
+    bound = want.abs() * (2.0 ** -8 + 34 * 2.0 ** -24)
+    assert bool(((got.double() - want).abs() <= bound)[ok].all())
+
+
 def test_norm_and_turn_of_odd_rows():
     """Rows of zeros (the norm's eps alone), very large and very small ones, an infinity and a NaN."""
     print("case: append4 of odd rows", flush=True)
