@@ -171,10 +171,10 @@ append4_kernel(int32_t B, int32_t n_q, int32_t Hq, const uint16_t* __restrict__ 
       inv = 1.0 / sqrt(lanes8_sum(ss) * (1.0 / kDim) + (double)eps);
     }
     {
-      // With u = 2^-24: a value after the norm is off by 1.5 u of itself (inv, inv w, the product), a cosine or sine by
-      // 1.6 u (its angle's rounding) and two steps, 2 u; a value turned by their sums in both products, 5.1 u, a product's
-      // rounding and its own: under 7 u (|a| + |b|).  12 u here; and where inv w is below the normal numbers, its 2^-150
-      // times the key.
+      // With u = 2^-24, and by |a| + |b|: a value after the norm is off by 3 u (inv, inv w, the product), a cosine or sine
+      // by 2.5 u (its angle's rounding, pi / 2 u, and sincospif: under 0.88 u for every float from -1 to 1, compared
+      // one by one with fp64), a product by its rounding, u, and the sum by its own, u: 7.5 u in all.  x - off and x + off
+      // are rounded once more, under 1.1 u.  12 u here; and where inv w is below the normal numbers, its 2^-150 times the key.
       open |= inv < 0x1p-126;
       float x[16], off[8];
 #pragma unroll

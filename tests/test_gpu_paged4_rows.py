@@ -375,3 +375,77 @@ def test_refusals_on_the_gpu():
         msa.msa_paged_read4(seven, seven, d["q_off"], d["page_table"], d["k_new"], d["v_new"])
     with pytest.raises(ValueError, match="v_out"):
         msa.msa_paged_read4(d["k_pages"], d["v_pages"], d["q_off"], d["page_table"], d["k_new"], d["v_new"][:, :1].contiguous())
+
+
+NEAR = 2.0 ** -40
+
+
+def candidates(n, positions, norm, turn, w, gen):
+    """Heads whose codes or scale bytes come out otherwise in fp32 than in 64 bits: of each position, among n random heads, up to 8
+    [8][128] bf16, those with another scale byte first (filled up with any others), how many they are, and how many of
+    them have another scale byte."""
+    f = torch.tensor([THETA ** (-e / 64.0) for e in range(64)], dtype=torch.float64).cuda()
+    w = w.cuda()
+    elements = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]).cuda()
+
+    def exponent(x):                              # exact in either width
+        m = x.unflatten(-1, (4, 32)).abs().amax(-1)
+        mant, e = torch.frexp(m)                  # m = mant 2^e, mant in [0.5, 1)
+        return e - 3 + (mant > 0.875).int()
+
+    def codes(x):
+        y = torch.ldexp(x.unflatten(-1, (4, 32)).abs(), -exponent(x)[..., None]).flatten(-2)
+        c = torch.zeros_like(y, dtype=torch.int32)
+        for i, v in enumerate(elements.tolist()):
+            c += (y >= v) if i % 2 else (y > v)
+        return c
+
+    for p in positions:
+        x = torch.randn(n, 128, generator=gen, device="cuda").to(BF16)
+        x64, x32 = x.double(), x.float()
+        if norm:
+            inv = 1.0 / torch.sqrt((x64 * x64).mean(-1, keepdim=True) + float(np.float32(EPS)))
+            x64, x32 = x64 * (inv * w.double()), x32 * (inv.float() * w.float())
+        if turn:
+            part = p * f / (2 * np.pi)
+            half = 2.0 * (part - torch.round(part))
+            pair = lambda y, c, s: torch.cat([y[:, :64] * c - y[:, 64:] * s, y[:, 64:] * c + y[:, :64] * s], 1)
+            x64 = pair(x64, torch.cos(np.pi * half), torch.sin(np.pi * half))
+            half = half.float().double()
+            x32 = pair(x32, torch.cos(np.pi * half).float(), torch.sin(np.pi * half).float())
+        other = (exponent(x64) != exponent(x32)).any(-1)
+        any_other = other | (codes(x64) != codes(x32)).any(-1)
+        rank = any_other.int() + other.int()
+        best, at = rank.sort(descending=True, stable=True)
+        yield x[at[:8]], int((best[:8] > 0).sum()), int((best[:8] > 1).sum())
+
+
+@pytest.mark.parametrize("norm,turn,n,least", [(True, True, 1 << 17, 200), (False, True, 1 << 17, 200), (True, False, 1 << 17, 100)])
+def test_codes_that_fp32_leaves_open(norm, turn, n, least):
+    """Keys next to borders of two codes or exponents, where arithmetic in fp32 falls to the other side: the bytes are those of 64
+    bits.  Every value is exact, or further from a border than 64 bits leave open (positions are below 256), so all bytes
+    count."""
+    print("case: append4, codes that fp32 leaves open", norm, turn, flush=True)
+    T = 256
+    b = Batch4([T], [T], page=16, hq=8, layers=1, seed=17)
+    gen = torch.Generator(device="cuda").manual_seed(17 + 2 * norm + turn)
+    found = scales = 0
+    for t, (rows, many, of_scales) in enumerate(candidates(n, range(T), norm, turn, b.w_k[0], gen)):
+        b.k_new[0, t] = rows.cpu()
+        found, scales = found + many, scales + of_scales
+    print("heads that differ in fp32: %d of %d, in a scale byte: %d" % (found, 8 * T, scales), flush=True)
+    assert found >= least and scales >= 1
+    w = b.w_k[0] if norm else None
+    want = {}
+    for t in range(T):
+        x, size = turned(b.k_new[0, t:t + 1], w, [t]) if turn else (b.k_new[0, t:t + 1].double(), None)
+        if not turn:
+            x = x / torch.sqrt((x * x).mean(-1, keepdim=True) + float(np.float32(EPS))) * w.double()
+            size = x.abs()
+        ends = quantise(x[0] - NEAR * size[0]), quantise(x[0] + NEAR * size[0])
+        exact = not norm and t == 0               # cosines of 1 and sines of 0: the keys as they are, on borders too
+        assert exact and torch.equal(x[0], b.k_new[0, t].double()) or torch.equal(ends[0][0], ends[1][0]) and torch.equal(ends[0][1], ends[1][1])
+        want[0, 0, t] = x[0], size[0]
+    d = b.to_device()
+    append(b, d, norm="k" if norm else "", q=False, theta=THETA if turn else 0.0)
+    check_pages(b, b.k_pages4, d["k_pages"].cpu(), want, 0.0)
