@@ -435,7 +435,8 @@ int msa_paged_attend(int32_t n_layers, int32_t B, int32_t n_groups, int32_t n_q,
  *   k_pages, v_pages  [n_layers][n_pages][page_tokens * MSA_ROW4_BYTES] uint8, 16-byte aligned.  A page is [8 heads]
  *                     [page_tokens][64] bytes of codes, dim 2 i in the low half of byte i, then [8][page_tokens][4]
  *                     bytes of scales; page_tokens a power of two up to MSA_MAX_PAGE_TOKENS.  Any bytes may be read
- *                     (scale bytes that the append does not write: 2^(byte - 127))
+ *                     (scale bytes that the append does not write: 2^(byte - 127), subnormal values among them;
+ *                     values past bf16's range are infinities)
  *
  * page_table, q_off, kv_len and the limits as for the cache in bf16. */
 #define MSA_ROW4_BYTES 544

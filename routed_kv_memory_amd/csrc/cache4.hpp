@@ -27,10 +27,11 @@ __device__ __forceinline__ int scales4_at(int head, int r, int shift) {
   return (kHeads * kCodes4 << shift) + ((head << shift) + r) * kBlocks4;
 }
 
-// A scale byte as the float that a conversion takes.
+// A scale byte as the float that a conversion takes: it looks at the exponent alone, so 0 is 2^-127 and 255 NaN.
 __device__ __forceinline__ float scale4(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// 8 codes as packed bf16, each the value it stands for.
+// 8 codes as packed bf16, each the value it stands for: exact, bf16's subnormal numbers (bytes 0 and 1) too; an infinity
+// past its range (bytes 253 and 254).
 __device__ __forceinline__ u32x4 values4(uint32_t codes, float scale) {
   u32x4 w;
   w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0));
