@@ -553,3 +553,18 @@ def test_no_tokens_and_refusals_on_the_gpu():
         args[at] = bad
         with pytest.raises(error):
             msa.msa_paged_attend4(*args)
+
+
+@pytest.mark.parametrize("page", [1, 16, 64])
+@pytest.mark.parametrize("local", [1, 31, 32, 33, 63, 64, 65, 95, 97, 128, 129])
+def test_ends_of_streamed_tiles(local, page):
+    """Streamed tiles are 64 local rows, used 32 at a time, or 16 memory rows: one and two tokens that end with, before and
+    behind them, and a shared part of as many rows."""
+    print("case: ends of streamed tiles, %d rows, pages of %d" % (local, page), flush=True)
+    memory = [0, 1, 15, 16, 17, 31, 32, 33]
+    new = [1, 2] * 4 + [1, 1]
+    rows = [max(n, local) for n in new[:8]] + [local + 65, local + 1]
+    b = Batch4(new, rows, groups=[1] * 8 + [2], ctx=[memory + [16]], pre=[0] * 8 + [local // page * page], page=page, hq=64,
+               seed=800 + local, q_std=2.0)
+    for dtype in (F32, BF16):
+        check(b, attend(b, dtype=dtype))
