@@ -10,14 +10,18 @@
 //   are loaded as the first product's A operand takes them (lane l: 32 dims, a block with its scale, of row l & 15) and
 //   turned into bf16 in registers; V's codes wait in the wave's LDS tile, so that their registers take the next
 //   tile's, and are turned into bf16 there 32 rows at a time.  Bound: HBM.  One token over 36,300 rows in 18 layers:
-//   201 us, 4.6 TB/s; 64 users' long conversations in one layer: 95 us, 4.0 TB/s.  A second tile of K on its way takes
-//   registers that are not there (232-278 us for then 209).
+//   195-202 us, 4.6-4.7 TB/s; 64 users' long conversations in one layer: 95 us, 4.0 TB/s (a plain read of as much
+//   reaches 5.8 to 6.2).  A second tile of K on its way takes registers that are not there (232-278 us for then 209).
 // - More columns: 4 waves share tiles of 32 rows, which are turned into bf16 on the way into LDS, four tiles a step,
 //   the next step's codes on their way meanwhile (loaded when they are needed: 273 us where this took 141,
 //   drafted tokens; 102-109 now).  Bound: matrix and vector units in turn.
 // - Four column blocks, over tiles that all columns see: a pipeline of its own, where each wave forms the next tile's
 //   scores beside this one's weights.  4,000 tokens over 32,300 rows: 2.16 ms, 1.04 PFLOP/s, matrix cores 47% busy while
-//   the clock falls to 2.07 GHz; 2.36 ms without it.  For two blocks it gains nothing.
+//   the clock falls to 2.07 GHz; 2.36 ms without it.  For two blocks it gains nothing.  It needs 16 rows in one page: pages
+//   of 4 or 8 rows take 2.38 ms where those of 16 to 256 take 2.21.
+//
+// One kernel for all of them has registers for none to spare: 16 vector registers spill with bf16 output, 22 with fp32 (68 and
+// 92 bytes of scratch a lane).
 #include "attend_core.hpp"
 #include "cache4.hpp"
 
@@ -26,7 +30,8 @@ namespace {
 
 // Costs: where all shares had as many tiles, those of memory rows ended after 128 us, those of local ones (four times
 // the softmax, and codes to turn) after 173 to 231; one token over 4,300 + 32,000 rows in 18 layers 201 us, 217 with equal
-// costs, 207 with 3 to 4, 202 with 3 to 5, 213 with 1 to 2.
+// costs, 207 with 3 to 4, 202 with 3 to 5, 213 with 1 to 2.  Elsewhere against equal costs: 4,300 + 4,300 rows 92.5 and
+// 106 us, 4,300 + 400 76 and 78.5, 16 users in four layers 173 and 179, 64 users in one 95.9 and 96.4.
 struct Rows4 {
   static constexpr int kStreamCtx = 16, kStreamLocal = 64, kCtxCost = 2, kLocalCost = 3;
   static constexpr bool kLongestFirst = true;
@@ -570,8 +575,10 @@ attend4_kernel(const AttendArgs a) {
     attend_streams<BF16_OUT>(a, n, p, sh.streams.seg, sh.streams.n_seg, reinterpret_cast<uint16_t*>(tile),
                              id - first_share, layer, tid);
   } else if (id >= first_item && id < first_item + p.all_items) {
-    // Items of one round, two a CU (workgroup i and i + the number of CUs): the longest that need not share have a CU each, of
-    // the others the longest and the shortest are side by side.  CUs then end within 85 to 98 us, 59 to 124 without.
+    // Items of one round, two a CU: the longest that need not share have a CU each, of the others the longest and the shortest
+    // are side by side.  CUs then end within 85 to 98 us, 59 to 124 without.  A pair is layers * (512 / layers / 2) workgroups
+    // apart, the number of CUs where the layers divide that, else a few less: sequences of drafted tokens in 1, 2 and 4 layers
+    // 103, 118 and 109 us (107, 123 and 113 unpaired), three in 18 layers 332 (334), 24 in one layer 57.6 (56.9).
     uint32_t item = id - first_item;
     const uint32_t cus = a.wgs / 2, n_items = p.all_items;
     if (p.all_cost == 0 && n_items > cus && n_items <= 2 * cus) {
